@@ -9,7 +9,9 @@ The low-level names mirror the C entry points (``gdn_plan_create_replay``,
 ``gdn_tail_replay_state``, ``gdn_tail_replay_outputs``, ``gdn_chunk_prefill``,
 ``gdn_decode_step``, ...).  ``ReplayPlan`` and
 ``PrefillPlan`` wrap a plan's lifetime; ``tail_replay_state`` and
-``chunk_prefill`` are the one-call conveniences on torch tensors.
+``chunk_prefill`` are the one-call conveniences on torch tensors.  The
+full-attention layers of the hybrid stack have ``qk_norm_rope`` and
+``PagedAttention`` (``paged_attention`` in one call).
 """
 from __future__ import annotations
 
@@ -27,6 +29,7 @@ LIB_PATH = os.path.join(_PKG, "libgdn_tail_replay_debug.so" if DEBUG_BOUNDS else
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT, \
     GDN_ERR_ALLOC, GDN_ERR_MISMATCH, GDN_ERR_BOUNDS = range(8)
 GDN_F32, GDN_BF16 = 0, 1
+GDN_ROTARY_HALVES, GDN_ROTARY_INTERLEAVED = 0, 1
 GDN_KERNEL_AUTO, GDN_KERNEL_RECURRENT, GDN_KERNEL_CHUNKED_TC = 0, 1, 2
 # the chunked kernel with the state-only replay pinned to its two-CTA-per-SM kernel (the
 # default), its warp-specialised one or its cluster-pair one
@@ -39,7 +42,7 @@ EXPORTED = (
     "gdn_workspace_status", "gdn_status_string", "gdn_version", "gdn_tail_replay_state_noalloc",
     "gdn_tail_replay_outputs", "gdn_decode_step", "gdn_plan_create_fused", "gdn_tail_replay_prefill",
     "gdn_selftest_bounded_wait", "gdn_debug_fail_plan_allocations", "gdn_selftest_index_check",
-    "gdn_debug_bounds_enabled",
+    "gdn_debug_bounds_enabled", "gdn_qk_norm_rope", "gdn_paged_attention", "gdn_paged_attention_workspace_bytes",
 )
 
 
@@ -59,6 +62,48 @@ class gdn_varlen_desc(ctypes.Structure):
         ("kernel", ctypes.c_int32),
         ("seq_offsets_host", ctypes.POINTER(ctypes.c_int32)),
         ("row_stride_elems", ctypes.c_int64),
+    ]
+
+
+class gdn_paged_kv(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class gdn_qk_desc(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("num_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("rotary_style", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("q_row_stride", ctypes.c_int64),
+        ("k_row_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64),
+    ]
+
+
+class gdn_attn_desc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("q_row_stride", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -93,6 +138,11 @@ def _load():
         "gdn_debug_fail_plan_allocations": (None, [I32]),
         "gdn_selftest_index_check": (I32, [P, P]),
         "gdn_debug_bounds_enabled": (I32, []),
+        "gdn_qk_norm_rope": (I32, [ctypes.POINTER(gdn_qk_desc), P, P, P, P, P, P, P, ctypes.c_float,
+                                   ctypes.POINTER(gdn_paged_kv), P, P, P, P, P, P]),
+        "gdn_paged_attention": (I32, [ctypes.POINTER(gdn_attn_desc), ctypes.POINTER(gdn_paged_kv), P, P, P, P, P, P,
+                                      P, P, P, P]),
+        "gdn_paged_attention_workspace_bytes": (ctypes.c_size_t, [I32, I32, I32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -351,6 +401,125 @@ def gdn_workspace_status(workspace, stream=None) -> int:
     return int(_lib.gdn_workspace_status(_ptr(workspace), _stream_handle(stream)))
 
 
+def _rows_of(t, heads, dim, name):
+    """Row stride (elements) of a [rows, heads, dim] view with contiguous heads inside a row."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [rows, {heads}, {dim}]")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name} must have contiguous heads inside a row")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _dense(t, shape, dtype, name):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _same_device(*tensors):
+    """Every tensor on the current CUDA device, where the call launches."""
+    import torch
+    here = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != here):
+            raise ValueError("every tensor must be on the current CUDA device")
+
+
+def _paged_kv(k_cache, v_cache):
+    """Descriptor of [num_pages, page_size, num_kv_heads, head_dim] key and value pools (any strides with
+    contiguous elements inside a head, the same for both)."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim], alike")
+    if k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+        raise ValueError("k_cache and v_cache must share their strides, with contiguous elements inside a head")
+    c = gdn_paged_kv()
+    c.num_pages, c.page_size, c.num_kv_heads, c.head_dim = k_cache.shape
+    c.dtype = _dtype_code(k_cache.dtype)
+    if not k_cache.is_contiguous():
+        c.page_stride, c.row_stride, c.head_stride = k_cache.stride()[:3]
+    return c
+
+
+def gdn_qk_norm_rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, k_cache, v_cache, slots, q_out, k_out,
+                     interleaved=False, stream=None):
+    """Norm, rotation and cache append (see ``qk_norm_rope``); every output is given."""
+    import torch
+    _same_device(q, k, v, positions, inv_freq, q_weight, k_weight, k_cache, v_cache, slots, q_out, k_out)
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q must be [rows, num_heads, head_dim] and k [rows, num_kv_heads, head_dim]")
+    rows, heads, dim = q.shape
+    kv = k.shape[1]
+    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+        raise ValueError("q, k and v must have one dtype")
+    d = gdn_qk_desc()
+    d.rows, d.num_heads, d.num_kv_heads, d.head_dim = rows, heads, kv, dim
+    d.rotary_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    d.rotary_style = GDN_ROTARY_INTERLEAVED if interleaved else GDN_ROTARY_HALVES
+    d.dtype = _dtype_code(q.dtype)
+    d.q_row_stride, d.k_row_stride = _rows_of(q, heads, dim, "q"), _rows_of(k, kv, dim, "k")
+    if inv_freq is not None:
+        _dense(inv_freq, (inv_freq.numel(),), torch.float64, "inv_freq")
+        _dense(positions, (rows,), torch.int64, "positions")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _dense(w, (dim,), torch.float32, name)
+    _dense(q_out, (rows, heads, dim), q.dtype, "q_out")
+    if k_out is not None:
+        _dense(k_out, (rows, kv, dim), q.dtype, "k_out")
+    cache = None
+    if k_cache is not None:
+        if v is None or v_cache is None or slots is None or v.shape[0] != rows:
+            raise ValueError("a cache needs v, v_cache and slots, one row of each per row of k")
+        d.v_row_stride = _rows_of(v, kv, dim, "v")
+        _dense(slots, (rows,), torch.int64, "slots")
+        c = _paged_kv(k_cache, v_cache)
+        if k_cache.dtype != q.dtype:
+            raise ValueError("the cache must have the dtype of q, k and v")
+        cache = ctypes.byref(c)
+    elif slots is not None or v_cache is not None:
+        raise ValueError("slots and v_cache need k_cache")
+    _check(_lib.gdn_qk_norm_rope(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v) if cache else None, _ptr(positions),
+                                 _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), eps, cache, _ptr(slots),
+                                 _ptr(k_cache), _ptr(v_cache), _ptr(q_out), _ptr(k_out), _stream_handle(stream)),
+           "gdn_qk_norm_rope")
+
+
+def gdn_paged_attention_workspace_bytes(dtype, head_dim, max_batch) -> int:
+    return int(_lib.gdn_paged_attention_workspace_bytes(_dtype_code(dtype), int(head_dim), int(max_batch)))
+
+
+def gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace, scale=None,
+                        window=0, stream=None):
+    """Causal attention of new tokens over a paged cache (see ``PagedAttention.run``)."""
+    import torch
+    _same_device(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace)
+    c = _paged_kv(k_cache, v_cache)
+    if q.dim() != 3 or q.dtype != k_cache.dtype:
+        raise ValueError("q must be [rows, num_heads, head_dim] of the cache's dtype")
+    rows, heads, dim = q.shape
+    if dim != c.head_dim:
+        raise ValueError("q and the cache must have one head_dim")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    batch = page_table.shape[0]
+    _dense(page_table, page_table.shape, torch.int32, "page_table")
+    _dense(cu_seqlens, (batch + 1,), torch.int32, "cu_seqlens")
+    _dense(context_len, (batch,), torch.int32, "context_len")
+    _dense(o_out, (rows, heads, dim), q.dtype, "o_out")
+    if lse_out is not None:
+        _dense(lse_out, (rows, heads), torch.float32, "lse_out")
+    need = _lib.gdn_paged_attention_workspace_bytes(c.dtype, dim, batch)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"the workspace must have at least {need} bytes")
+    d = gdn_attn_desc()
+    d.batch, d.num_heads, d.rows, d.q_row_stride = batch, heads, rows, _rows_of(q, heads, dim, "q")
+    d.max_pages, d.window = page_table.shape[1], int(window)
+    d.scale = dim ** -0.5 if scale is None else scale
+    _check(_lib.gdn_paged_attention(ctypes.byref(d), ctypes.byref(c), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                    _ptr(page_table), _ptr(cu_seqlens), _ptr(context_len), _ptr(o_out), _ptr(lse_out),
+                                    _ptr(workspace), _stream_handle(stream)),
+           "gdn_paged_attention")
+
+
 class _Plan:
     def __init__(self, handle, H, dk, dv, dtype, batch):
         import torch
@@ -465,3 +634,72 @@ def decode_step(q, k, v, alpha, beta, state, o=None, in_place=True):
     out = state if in_place else torch.empty_like(state)
     gdn_decode_step(q, k, v, alpha, beta, state, out, o)
     return o, out
+
+
+class PagedAttention:
+    """Causal attention of new tokens over a paged key/value cache, with the workspace that its calls share
+    (calls that may run at the same time, or captured ones that may, need one each).
+
+    Lengths and pages are device tensors read when the call runs, so a captured ``run`` may be replayed with new
+    ones.  The cache already holds the new tokens (``qk_norm_rope`` appends them).
+    """
+
+    def __init__(self, num_heads, num_kv_heads, head_dim, dtype, max_batch, max_rows=None):
+        import torch
+        self.num_heads, self.num_kv_heads, self.head_dim = int(num_heads), int(num_kv_heads), int(head_dim)
+        self.dtype, self.max_batch = _dtype_code(dtype), int(max_batch)
+        self.max_rows = None if max_rows is None else int(max_rows)
+        n = gdn_paged_attention_workspace_bytes(dtype, head_dim, max_batch)
+        if n == 0 or num_kv_heads < 1 or num_heads < 1 or num_heads % num_kv_heads:
+            raise GdnError(GDN_ERR_UNSUPPORTED, "PagedAttention")
+        self.workspace = torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+    def run(self, q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out=None, scale=None, window=0,
+            stream=None, workspace=None):
+        """q [rows, H, d] (row-strided views too); k_cache, v_cache [num_pages, page_size, Hkv, d]; page_table
+        [B, max_pages], cu_seqlens [B + 1], context_len [B] int32; o_out [rows, H, d] and lse_out [rows, H] fp32
+        are written at the rows that sequences own.  Row i of a sequence with n new tokens and context L is
+        position L - n + i and sees the keys up to it, with a window only the last `window` of them."""
+        if q.shape[1:] != (self.num_heads, self.head_dim) or k_cache.shape[2] != self.num_kv_heads:
+            raise ValueError("q or the cache has other heads than this PagedAttention")
+        if page_table.shape[0] > self.max_batch or (self.max_rows is not None and q.shape[0] > self.max_rows):
+            raise ValueError("more sequences or rows than this PagedAttention was made for")
+        gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out,
+                            self.workspace if workspace is None else workspace, scale, window, stream)
+
+    def status(self, stream=None) -> int:
+        return gdn_workspace_status(self.workspace, stream)
+
+    def check(self, stream=None):
+        _check(self.status(stream), "device status")
+
+
+def paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len, scale=None, window=0, with_lse=False):
+    """One-shot paged attention; returns o [rows, H, d], or (o, lse) with `with_lse`.  Rows that no sequence owns
+    are zero (lse -inf)."""
+    import torch
+    attn = PagedAttention(q.shape[1], k_cache.shape[2], q.shape[2], q.dtype, page_table.shape[0])
+    o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.full(q.shape[:2], float("-inf"), dtype=torch.float32, device=q.device) if with_lse else None
+    attn.run(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o, lse, scale, window)
+    attn.check()
+    return (o, lse) if with_lse else o
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, v=None,
+                 k_cache=None, v_cache=None, slots=None, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head (where its weight is given), rotation of the first
+    2 * inv_freq.numel() elements by position * inv_freq (fp64, radians), and, with a paged cache, the append of
+    keys and values at `slots` (int64 page * page_size + row; a negative one writes nothing).
+
+    q, k and v are [rows, heads, d] (row-strided views too).  Returns (q_out, k_out); k_out is made only where
+    there is no cache and none was given."""
+    import torch
+    with torch.cuda.stream(stream):   # what is made here is made on the stream that fills it
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None and k_cache is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    gdn_qk_norm_rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, k_cache, v_cache, slots, q_out, k_out,
+                     interleaved, stream)
+    return q_out, k_out

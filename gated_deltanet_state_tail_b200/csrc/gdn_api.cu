@@ -9,11 +9,13 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <new>
 #include <vector>
 
+#include "gdn_attn.h"
 #include "gdn_internal.h"
 #include "gdn_tail_replay.h"
 
@@ -284,6 +286,39 @@ void fill_common(gdn_plan_t plan, CallArgs& a, void* workspace) {
     a.replay_variant = plan->replay_variant;
 }
 
+// A paged cache descriptor and the strides that it implies (elements).
+struct CacheStrides {
+    long long page, row, head;
+};
+
+gdn_status check_paged_kv(const gdn_paged_kv* c, CacheStrides* st) {
+    if (!c) return GDN_ERR_INVALID_ARG;
+    if (c->dtype != GDN_F32 && c->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128) return GDN_ERR_UNSUPPORTED;
+    if (c->num_pages < 1 || c->num_kv_heads < 1 || c->page_size < 1) return GDN_ERR_INVALID_ARG;
+    if (c->page_size % 8 != 0) return GDN_ERR_UNSUPPORTED;
+    const long long d = c->head_dim, vec = c->dtype == GDN_BF16 ? 8 : 4;
+    if (c->page_stride == 0 && c->row_stride == 0 && c->head_stride == 0) {
+        const long long row = c->num_kv_heads * d;
+        *st = CacheStrides{row * c->page_size, row, d};
+    } else {
+        *st = CacheStrides{c->page_stride, c->row_stride, c->head_stride};
+    }
+    for (const long long s : {st->page, st->row, st->head})
+        if (s < d || s % vec != 0 || s > (1ll << 37)) return GDN_ERR_INVALID_ARG;
+    // element offsets are 64-bit; the last one must fit comfortably
+    const double last = (double)c->num_pages * (double)st->page + (double)c->page_size * (double)st->row +
+                        (double)c->num_kv_heads * (double)st->head;
+    if (last > (double)(1ll << 46)) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+// A row stride argument: 0 = packed, else at least `width` elements and a multiple of 16 bytes.
+bool row_stride_ok(long long* stride, long long width, int dtype) {
+    if (*stride == 0) *stride = width;
+    return *stride >= width && *stride % (dtype == GDN_BF16 ? 8 : 4) == 0 && *stride <= (1ll << 37);
+}
+
 }  // namespace
 
 extern "C" {
@@ -510,6 +545,154 @@ gdn_status gdn_decode_step(int32_t batch, int32_t num_heads, int32_t d_k, int32_
     return GDN_OK;
 }
 
+gdn_status gdn_qk_norm_rope(const gdn_qk_desc* d, const void* q, const void* k, const void* v,
+                            const int64_t* positions, const double* inv_freq, const float* q_weight,
+                            const float* k_weight, float eps, const gdn_paged_kv* cache, const int64_t* slots,
+                            void* k_pages, void* v_pages, void* q_out, void* k_out, void* stream) {
+    if (!d || d->rows < 0 || d->num_heads < 1 || d->num_kv_heads < 1) return GDN_ERR_INVALID_ARG;
+    if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+    if (d->head_dim != 64 && d->head_dim != 128) return GDN_ERR_UNSUPPORTED;
+    if (d->rotary_dim < 0 || d->rotary_dim > d->head_dim) return GDN_ERR_INVALID_ARG;
+    if (d->rotary_dim % 16 != 0) return GDN_ERR_UNSUPPORTED;
+    if (d->rotary_style != GDN_ROTARY_HALVES && d->rotary_style != GDN_ROTARY_INTERLEAVED) return GDN_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return GDN_ERR_INVALID_ARG;
+    const long long D = d->head_dim;
+    long long rs_q = d->q_row_stride, rs_k = d->k_row_stride, rs_v = d->v_row_stride;
+    if (!row_stride_ok(&rs_q, d->num_heads * D, d->dtype) || !row_stride_ok(&rs_k, d->num_kv_heads * D, d->dtype) ||
+        !row_stride_ok(&rs_v, d->num_kv_heads * D, d->dtype))
+        return GDN_ERR_INVALID_ARG;
+    if (d->num_heads > (1 << 20) || d->num_kv_heads > (1 << 20)) return GDN_ERR_INVALID_ARG;
+    if (d->rows > 0x7fffffffll) return GDN_ERR_INVALID_ARG;   // grid x
+    const long long widest = std::max(rs_q, std::max(rs_k, rs_v));
+    if (d->rows > 0 && widest > (1ll << 46) / d->rows) return GDN_ERR_INVALID_ARG;
+    CacheStrides st{0, 0, 0};
+    if (cache) {
+        const gdn_status s = check_paged_kv(cache, &st);
+        if (s != GDN_OK) return s;
+        if (cache->dtype != d->dtype || cache->num_kv_heads != d->num_kv_heads || cache->head_dim != d->head_dim)
+            return GDN_ERR_INVALID_ARG;
+    }
+    if (d->rows == 0) return GDN_OK;
+    if (!q || !k || !q_out || (!cache && !k_out)) return GDN_ERR_INVALID_ARG;
+    if (d->rotary_dim > 0 && (!positions || !inv_freq)) return GDN_ERR_INVALID_ARG;
+    if (cache && (!v || !slots || !k_pages || !v_pages)) return GDN_ERR_INVALID_ARG;
+    if (!cache && (slots || k_pages || v_pages)) return GDN_ERR_INVALID_ARG;
+    for (const void* p : {q, k, v, (const void*)positions, (const void*)inv_freq, (const void*)q_weight,
+                          (const void*)k_weight, (const void*)slots, (const void*)k_pages, (const void*)v_pages,
+                          (const void*)q_out, (const void*)k_out})
+        if (p && !aligned16(p)) return GDN_ERR_INVALID_ARG;
+    // in place: the outputs are packed, so an input that is its own output must be
+    if ((q_out == q && rs_q != d->num_heads * D) || (k_out == k && rs_k != d->num_kv_heads * D))
+        return GDN_ERR_INVALID_ARG;
+    gdn::NormRopeArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.dtype = d->dtype;
+    a.num_heads = d->num_heads;
+    a.num_kv_heads = d->num_kv_heads;
+    a.dim = d->head_dim;
+    a.rotary_dim = d->rotary_dim;
+    a.interleaved = d->rotary_style == GDN_ROTARY_INTERLEAVED;
+    a.rows = d->rows;
+    a.rs_q = rs_q;
+    a.rs_k = rs_k;
+    a.rs_v = rs_v;
+    a.eps = eps;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.positions = reinterpret_cast<const long long*>(positions);
+    a.inv_freq = inv_freq;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    if (cache) {
+        a.slots = reinterpret_cast<const long long*>(slots);
+        a.k_pages = k_pages;
+        a.v_pages = v_pages;
+        a.num_pages = cache->num_pages;
+        a.page_size = cache->page_size;
+        a.page_stride = st.page;
+        a.cache_row_stride = st.row;
+        a.cache_head_stride = st.head;
+    }
+    if (gdn::launch_norm_rope(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+size_t gdn_paged_attention_workspace_bytes(int32_t dtype, int32_t head_dim, int32_t max_batch) {
+    if ((dtype != GDN_F32 && dtype != GDN_BF16) || (head_dim != 64 && head_dim != 128) || max_batch < 0) return 0;
+    return gdn::paged_attention_layout(dtype, head_dim, max_batch).bytes;
+}
+
+gdn_status gdn_paged_attention(const gdn_attn_desc* d, const gdn_paged_kv* cache, const void* q, const void* k_pages,
+                               const void* v_pages, const int32_t* page_table, const int32_t* cu_seqlens,
+                               const int32_t* context_len, void* o_out, float* lse_out, void* workspace,
+                               void* stream) {
+    if (!d) return GDN_ERR_INVALID_ARG;
+    CacheStrides st;
+    const gdn_status s = check_paged_kv(cache, &st);
+    if (s != GDN_OK) return s;
+    if (d->batch < 0 || d->rows < 0 || d->rows > 0x7fffffffll || d->num_heads < 1) return GDN_ERR_INVALID_ARG;
+    if (d->num_heads % cache->num_kv_heads != 0) return GDN_ERR_INVALID_ARG;
+    if (d->num_heads / cache->num_kv_heads > 64) return GDN_ERR_UNSUPPORTED;
+    if (d->window < 0 || !(d->scale > 0.0f) || std::isinf(d->scale)) return GDN_ERR_INVALID_ARG;
+    long long rs_q = d->q_row_stride;
+    if (!row_stride_ok(&rs_q, (long long)d->num_heads * cache->head_dim, cache->dtype)) return GDN_ERR_INVALID_ARG;
+    if (d->rows > 0 && rs_q > (1ll << 46) / d->rows) return GDN_ERR_INVALID_ARG;
+    if (d->max_pages < 1) return GDN_ERR_INVALID_ARG;
+    if (d->batch == 0 || d->rows == 0) return GDN_OK;
+    for (const void* p : {q, k_pages, v_pages, (const void*)page_table, (const void*)cu_seqlens,
+                          (const void*)context_len, (const void*)o_out, (const void*)workspace})
+        if (!p || !aligned16(p)) return GDN_ERR_INVALID_ARG;
+    if (lse_out && !aligned16(lse_out)) return GDN_ERR_INVALID_ARG;
+    if (o_out == q) return GDN_ERR_INVALID_ARG;   // a row's queries are read after other heads are written
+    gdn::attn::Args a;
+    std::memset(&a, 0, sizeof a);
+    a.dtype = cache->dtype;
+    a.batch = d->batch;
+    a.num_heads = d->num_heads;
+    a.num_kv_heads = cache->num_kv_heads;
+    a.group = d->num_heads / cache->num_kv_heads;
+    a.dim = cache->head_dim;
+    a.page_size = cache->page_size;
+    a.num_pages = cache->num_pages;
+    a.max_pages = d->max_pages;
+    a.shape = gdn::paged_attention_shape(cache->dtype, cache->head_dim);
+    a.block_tokens = a.shape.sub_rows / a.group;
+    a.rows = d->rows;
+    a.rs_q = rs_q;
+    a.page_stride = st.page;
+    a.row_stride = st.row;
+    a.head_stride = st.head;
+    a.scale = d->scale;
+    a.window = d->window;
+    a.q = q;
+    a.k = k_pages;
+    a.v = v_pages;
+    a.page_table = page_table;
+    a.cu = cu_seqlens;
+    a.ctx = context_len;
+    a.o = o_out;
+    a.lse = lse_out;
+    a.epoch = gdn::next_call_number();
+    const gdn::attn::Layout lay = gdn::paged_attention_layout(cache->dtype, cache->head_dim, d->batch);
+    char* w = static_cast<char*>(workspace);
+    a.ws = reinterpret_cast<WorkspaceHeader*>(w);
+    a.line = reinterpret_cast<gdn::attn::Line*>(w + lay.line);
+    a.seqs = reinterpret_cast<gdn::attn::Seq*>(w + lay.seqs);
+    a.part_lse = reinterpret_cast<float*>(w + lay.part_lse);
+    a.part_o = reinterpret_cast<float*>(w + lay.part_o);
+    if (gdn::launch_paged_attention(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
 gdn_status gdn_chunk_prefill(gdn_plan_t plan, const void* q, const void* k, const void* v,
                              const float* alpha, const float* beta, const int32_t* cu_seqlens,
                              const float* state_in, void* o_out, float* state_out,
@@ -650,12 +833,12 @@ const char* gdn_status_string(gdn_status s) {
         case GDN_ERR_CUDA: return "CUDA error";
         case GDN_ERR_TIMEOUT: return "device wait timed out";
         case GDN_ERR_ALLOC: return "allocation failed";
-        case GDN_ERR_MISMATCH: return "device descriptor arrays disagree with the plan";
+        case GDN_ERR_MISMATCH: return "device descriptor arrays disagree with the plan or the call";
         case GDN_ERR_BOUNDS: return "device index outside the plan's extents (debug build)";
     }
     return "unknown status";
 }
 
-int32_t gdn_version(void) { return 300; }
+int32_t gdn_version(void) { return 400; }
 
 }  // extern "C"

@@ -1,0 +1,202 @@
+// gdn_attn.h -- paged attention: the call's arguments and the schedule that its kernels
+// share.  Not part of the public ABI.
+//
+// The work is cut by key tiles.  A unit is a block of consecutive new tokens of one
+// sequence with the query heads of one key head (rows = tokens x heads of the group);
+// its cost is the number of key tiles that its causal (and window) range touches.  The
+// units' tiles, in the order (sequence, key head, token block), form one line of `total`
+// tiles, and each of `parts` CTAs takes the same length of it, wherever units begin and
+// end.  So one long context with one new token and a thousand short ones both fill the
+// GPU.  A CTA that holds a unit whole writes its outputs; a unit that the cuts split
+// leaves normalised partial outputs and log-sums, merged by the combine kernel in the
+// order of the line: the result does not depend on which CTA ran first.
+//
+// The lengths are read on the device (a captured call may be replayed with new ones), so
+// a one-block kernel builds the line: per sequence its checked lengths and the tiles
+// before it.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace attn {
+
+// One sequence of the line, 32 bytes.
+struct Seq {
+    int row0;            // first row of its new tokens in q and o
+    int qlen;            // new tokens; 0 if its descriptor entries are bad
+    int ctx;             // context length, the new tokens included
+    int pad;
+    long long head_tiles; // key tiles of one key head, over its token blocks
+    long long before;    // tiles of the sequences before it
+};
+static_assert(sizeof(Seq) == 32, "Seq is 32 bytes");
+
+// The line, in the workspace after the status header.
+struct Line {
+    long long total;     // tiles
+    long long per_part;  // tiles of each CTA (the last may have fewer)
+    int parts;           // CTAs with work
+    int pad[59];
+};
+static_assert(sizeof(Line) == 256, "Line is 256 bytes");
+
+// Sizes that a kernel family fixes.
+struct Shape {
+    int sub_rows;        // rows of one row tile
+    int subs;            // row tiles of a unit
+    int tile_keys;       // keys of a tile
+    int max_parts;       // CTAs of the grid
+    int min_tiles;       // least tiles of a CTA, so that splitting pays
+};
+
+struct Args {
+    int dtype, batch, num_heads, num_kv_heads, group, dim;
+    int page_size, num_pages, max_pages;    // max_pages: entries per row of the page table
+    int block_tokens;                       // tokens of a row tile: sub_rows / group
+    Shape shape;
+    long long rows;                         // rows of q and o
+    long long rs_q;
+    long long page_stride, row_stride, head_stride;
+    float scale;                            // of the scores
+    int window;                             // keys that a row sees at most; 0 = all
+    const void* q;
+    const void* k;
+    const void* v;
+    const int* page_table;                  // [batch, max_pages]
+    const int* cu;                          // [batch + 1]
+    const int* ctx;                         // [batch]
+    void* o;                                // [rows, num_heads, dim] packed
+    float* lse;                             // [rows, num_heads] or null
+    WorkspaceHeader* ws;
+    unsigned int epoch;
+    Line* line;
+    Seq* seqs;                              // [batch]
+    float* part_lse;                        // [2 * max_parts][subs * sub_rows], base 2
+    float* part_o;                          // [2 * max_parts][subs * sub_rows][dim]
+};
+
+__device__ __forceinline__ void report(const Args& a, unsigned int bits) {
+    tag_merge(&a.ws->status, a.epoch, bits, false);
+}
+
+// The key range and tiles of token block t of a sequence.
+struct Range {
+    int tok0, toks;      // first new token of the block and their number
+    int lo, hi;          // keys seen by at least one of its rows: [lo, hi)
+    int tile0, tiles;    // key tiles; at least one, so that rows without keys are written too
+};
+
+__device__ __forceinline__ Range block_range(const Args& a, int qlen, int ctx, int t) {
+    Range r;
+    const int step = a.block_tokens * a.shape.subs;
+    r.tok0 = t * step;
+    r.toks = min(step, qlen - r.tok0);
+    const int first = ctx - qlen + r.tok0;           // position of the first row (may be negative)
+    r.hi = max(0, first + r.toks);
+    r.lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
+    r.lo = min(r.lo, r.hi);
+    r.tile0 = r.lo / a.shape.tile_keys;
+    r.tiles = max(1, (r.hi + a.shape.tile_keys - 1) / a.shape.tile_keys - r.tile0);
+    return r;
+}
+
+__device__ __forceinline__ int token_blocks(const Args& a, int qlen) {
+    const int step = a.block_tokens * a.shape.subs;
+    return (qlen + step - 1) / step;
+}
+
+// A unit and its place on the line.
+struct Unit {
+    int b, head, t;      // sequence, key head, token block
+    Range r;
+    Seq s;
+    long long begin;     // tile of the line where it begins
+};
+
+// The unit that holds tile `pos` of the line (0 <= pos < total), by a whole warp.
+__device__ __forceinline__ Unit find_unit(const Args& a, long long pos) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.batch;                        // the last sequence with before <= pos is in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int i = lo + lane * step;
+        const bool below = i < hi && a.seqs[i].before <= pos;
+        const int n = __popc(__ballot_sync(0xffffffffu, below));   // lane 0 is always below
+        lo = lo + (n - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    Unit u;
+    u.b = lo;
+    u.s = a.seqs[lo];
+    const long long in = pos - u.s.before;
+    u.head = (int)(in / u.s.head_tiles);
+    const long long rem = in - u.head * u.s.head_tiles;
+    const int blocks = token_blocks(a, u.s.qlen);
+    long long done = 0;
+    for (int t0 = 0;; t0 += 32) {                    // ends: rem < head_tiles = the sum over all blocks
+        const int t = t0 + lane;
+        const int n = t < blocks ? block_range(a, u.s.qlen, u.s.ctx, t).tiles : 0;
+        int incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, done + incl > rem);
+        if (hit || t0 + 32 >= blocks) {
+            const int l = hit ? __ffs(hit) - 1 : 31;
+            u.t = t0 + l;
+            u.begin = u.s.before + u.head * u.s.head_tiles + done +
+                      __shfl_sync(0xffffffffu, incl - n, l);
+            break;
+        }
+        done += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    u.r = block_range(a, u.s.qlen, u.s.ctx, u.t);
+    return u;
+}
+
+// The unit after u on the line (the caller knows that there is one).
+__device__ __forceinline__ void next_unit(const Args& a, Unit& u) {
+    u.begin += u.r.tiles;
+    if (++u.t >= token_blocks(a, u.s.qlen)) {
+        u.t = 0;
+        if (++u.head >= a.num_kv_heads) {
+            u.head = 0;
+            do {
+                ++u.b;
+                if (u.b >= a.batch) return;
+                u.s = a.seqs[u.b];
+            } while (u.s.qlen == 0);
+        }
+    }
+    u.r = block_range(a, u.s.qlen, u.s.ctx, u.t);
+}
+
+// Where a CTA leaves its part of a split unit: two slots per CTA, one for the unit that its
+// stretch of the line begins with and one for the unit that it ends with.
+__device__ __forceinline__ long long part_slot(long long part, bool begins_stretch) {
+    return 2 * part + (begins_stretch ? 0 : 1);
+}
+
+cudaError_t launch_simt(const Args& a, cudaStream_t stream);
+Shape shape_simt(int dim);
+
+}  // namespace attn
+
+// Byte offsets of a call's workspace: status header, line, sequences, partial results.
+namespace attn {
+struct Layout {
+    size_t line, seqs, part_lse, part_o, bytes;
+};
+}  // namespace attn
+
+cudaError_t launch_paged_attention(const attn::Args& a, cudaStream_t stream);
+attn::Shape paged_attention_shape(int dtype, int dim);
+attn::Layout paged_attention_layout(int dtype, int dim, int batch);
+
+}  // namespace gdn

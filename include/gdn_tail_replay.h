@@ -66,7 +66,7 @@ typedef enum gdn_status {
     GDN_ERR_CUDA = 3,         /* a CUDA runtime call or launch failed */
     GDN_ERR_TIMEOUT = 4,      /* a device-side wait gave up (reported via the workspace) */
     GDN_ERR_ALLOC = 5,        /* plan creation could not allocate */
-    GDN_ERR_MISMATCH = 6,     /* device descriptor arrays disagree with the plan */
+    GDN_ERR_MISMATCH = 6,     /* device descriptor arrays disagree with the plan (or the call's extents) */
     GDN_ERR_BOUNDS = 7        /* debug build: a device index fell outside the plan's extents */
 } gdn_status;
 
@@ -257,6 +257,138 @@ GDN_API gdn_status gdn_decode_step(int32_t batch, int32_t num_heads, int32_t d_k
                                    int32_t dtype, const void* q, const void* k, const void* v,
                                    const float* alpha, const float* beta, const float* state_in,
                                    float* state_out, void* o_out, void* stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * The full-attention layers of the hybrid stack.  At a prefix-cache hit the
+ * same suffix that continues the rebuilt GDN states also goes through the
+ * stack's full-attention layers, whose keys and values sit in a paged cache
+ * ("Mecanismos Principais": the full-attention cache is copied back while
+ * the GDN states are replayed).  gdn_qk_norm_rope prepares the new tokens'
+ * queries and keys and appends keys and values to the cache;
+ * gdn_paged_attention lets the new tokens attend over it.  Both serve whole
+ * prompts, suffixes and single tokens, take no plan, read lengths, positions
+ * and page numbers on the device (a captured call may be replayed with new
+ * ones), allocate nothing and launch on `stream` of the current device, where
+ * every buffer lives.  Inference only, like the rest of the library.
+ *
+ * A paged cache: keys and values in two buffers of the same layout,
+ * [num_pages, page_size, num_kv_heads, head_dim] with the strides below.  A
+ * pool laid out head first, or one buffer for both, is described by strides.
+ */
+typedef struct gdn_paged_kv {
+    int32_t num_pages;     /* >= 1 */
+    int32_t page_size;     /* rows of a page; a multiple of 8 (else UNSUPPORTED) */
+    int32_t num_kv_heads;  /* >= 1 */
+    int32_t head_dim;      /* 64 or 128 */
+    int32_t dtype;         /* gdn_dtype */
+    int32_t reserved;      /* 0 */
+    int64_t page_stride;   /* elements between pages, rows and heads; all three 0 = */
+    int64_t row_stride;    /*   packed; else each >= head_dim and a multiple of 16 bytes */
+    int64_t head_stride;
+} gdn_paged_kv;
+
+typedef enum gdn_rotary_style {
+    GDN_ROTARY_HALVES = 0,      /* pairs (i, i + rotary_dim / 2) */
+    GDN_ROTARY_INTERLEAVED = 1  /* pairs (2 i, 2 i + 1) */
+} gdn_rotary_style;
+
+typedef struct gdn_qk_desc {
+    int64_t rows;          /* new tokens, >= 0 (0 launches nothing) */
+    int32_t num_heads;     /* query heads, >= 1 */
+    int32_t num_kv_heads;  /* key/value heads, >= 1 */
+    int32_t head_dim;      /* 64 or 128 */
+    int32_t rotary_dim;    /* leading elements that are rotated: 0 .. head_dim, a multiple of 16 */
+    int32_t rotary_style;  /* gdn_rotary_style */
+    int32_t dtype;         /* gdn_dtype of q, k, v, the outputs and the cache */
+    int64_t q_row_stride;  /* elements between rows of q, k and v; 0 = packed, else at least */
+    int64_t k_row_stride;  /*   heads * head_dim and a multiple of 16 bytes: q, k and v may be */
+    int64_t v_row_stride;  /*   slices of one projection buffer */
+} gdn_qk_desc;
+
+/*
+ * Norm and rotation of the new tokens' queries and keys, and their append to
+ * the cache, in one pass.  Per head: y = x rsqrt(mean(x^2) + eps) w, then each
+ * pair (a, b) of the rotated elements turns by t = position * inv_freq:
+ * (a cos t - b sin t, b cos t + a sin t).  Computed in fp32 and rounded once;
+ * angles are exact to fp32 at any position (no table).
+ *   q            [rows, num_heads, head_dim] (row stride of the descriptor)
+ *   k, v         [rows, num_kv_heads, head_dim]; v with a cache only.
+ *   positions    [rows] int64;  inv_freq [rotary_dim / 2] fp64, radians per
+ *                position (scaled frequencies as the model has them).  Both
+ *                may be NULL when rotary_dim = 0.
+ *   q_weight, k_weight
+ *                [head_dim] fp32, or NULL: that tensor is rotated only.
+ *   eps          finite, >= 0.
+ *   cache        NULL, or the descriptor of k_pages and v_pages; with it
+ *                slots [rows] int64: row r goes to row slots[r] % page_size of
+ *                page slots[r] / page_size, keys rotated, values as they are.
+ *                A negative slot or one past the pool writes nothing
+ *                (padding rows).  Slots of one call should be distinct: of rows
+ *                that share one, either one's elements may stay.
+ *   q_out        [rows, num_heads, head_dim] packed; may be q if q is packed.
+ *   k_out        [rows, num_kv_heads, head_dim] packed, or NULL with a cache;
+ *                may be k if k is packed.  Other overlaps are not allowed.
+ * Returns GDN_OK, INVALID_ARG, UNSUPPORTED (head_dim, rotary_dim, page_size or
+ * dtype) or CUDA.  It waits on nothing, so it has no workspace.
+ */
+GDN_API gdn_status gdn_qk_norm_rope(const gdn_qk_desc* desc, const void* q, const void* k, const void* v,
+                                    const int64_t* positions, const double* inv_freq, const float* q_weight,
+                                    const float* k_weight, float eps, const gdn_paged_kv* cache,
+                                    const int64_t* slots, void* k_pages, void* v_pages, void* q_out,
+                                    void* k_out, void* stream);
+
+typedef struct gdn_attn_desc {
+    int32_t batch;         /* sequences, >= 0 */
+    int32_t num_heads;     /* query heads: a multiple of num_kv_heads, at most 64 per key head */
+    int64_t rows;          /* rows of q, o_out and lse_out: 0 .. 2^31 - 1 */
+    int64_t q_row_stride;  /* elements between rows of q; 0 = packed (as in gdn_qk_desc) */
+    int32_t max_pages;     /* entries per row of the page table, >= 1 */
+    int32_t window;        /* keys a token sees at most, itself included; 0 = all */
+    float scale;           /* of the scores; finite, > 0 (commonly head_dim^-0.5) */
+    int32_t reserved;      /* 0 */
+} gdn_attn_desc;
+
+/* Bytes of device workspace of a gdn_paged_attention call with up to max_batch
+ * sequences (0 for an unsupported dtype or head_dim or a negative max_batch).
+ * It needs no initialisation.  Calls that may run at the same time, captured
+ * ones included, need separate workspaces. */
+GDN_API size_t gdn_paged_attention_workspace_bytes(int32_t dtype, int32_t head_dim, int32_t max_batch);
+
+/*
+ * Causal attention of new tokens over a paged cache that already holds their
+ * keys and values.  Sequence b owns rows [cu_seqlens[b], cu_seqlens[b+1]) of q;
+ * with n such rows and L = context_len[b], row i is position p = L - n + i and
+ * sees the keys j of max(0, p - window + 1) .. p (window 0: 0 .. p):
+ *   o = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j).
+ * A row that sees no key (L = 0, or more rows than context) gets o = 0 and
+ * lse = -infinity.  Cache rows outside the context or before every row's window
+ * are not used, whatever they hold, and page numbers of pages that hold only
+ * such rows are not read.  A key that some row of a sequence sees must have
+ * finite values in v.
+ *   q            [rows, num_heads, head_dim] (row stride of the descriptor)
+ *   page_table   [batch, max_pages] int32: page of key j of sequence b is
+ *                page_table[b][j / page_size].
+ *   cu_seqlens   [batch + 1] int32, non-decreasing, within 0 .. rows; rows
+ *                that no sequence owns are left untouched.
+ *   context_len  [batch] int32, 0 .. max_pages * page_size.
+ *   o_out        [rows, num_heads, head_dim] packed, the cache's dtype; not q.
+ *   lse_out      [rows, num_heads] fp32 (natural log), or NULL.
+ *   workspace    gdn_paged_attention_workspace_bytes(dtype, head_dim, batch).
+ * These arrays are checked on the device: a sequence whose offsets or context
+ * do not fit is skipped (its rows stay untouched), a page number outside
+ * 0 .. num_pages - 1 reads as zeros, and either sets GDN_ERR_MISMATCH in the
+ * workspace status; over replays of one captured call the status accumulates.
+ * batch = 0 or rows = 0 launches nothing.  bf16 runs on the tensor cores with
+ * the softmax in fp32 and its weights rounded to bf16; fp32 on the CUDA cores in
+ * fp32 throughout.  Reruns give identical bits.
+ * Returns GDN_OK, INVALID_ARG, UNSUPPORTED (dtype, head_dim, page_size, group)
+ * or CUDA; device-side problems are read with gdn_workspace_status().
+ */
+GDN_API gdn_status gdn_paged_attention(const gdn_attn_desc* desc, const gdn_paged_kv* cache, const void* q,
+                                       const void* k_pages, const void* v_pages, const int32_t* page_table,
+                                       const int32_t* cu_seqlens, const int32_t* context_len, void* o_out,
+                                       float* lse_out, void* workspace, void* stream);
 
 /*
  * Chunked prefill over each sequence of a prefill plan, continuing from

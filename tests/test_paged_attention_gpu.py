@@ -1,0 +1,303 @@
+"""gdn_paged_attention against a plain 64-bit implementation: lengths from none to long, groups, pages, windows,
+strides, and what the device checks refuse.  Bounds: tests/hybrid_reference.py."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import gated_deltanet_state_tail_b200 as gdn
+import hybrid_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+SENTINEL = 77.0
+
+
+def _queries(new, heads, d, dtype, seed, scale=1.0, strided=False):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1000 + seed)
+    rows = sum(new)
+    if strided:   # the first heads of a wider projection
+        wide = torch.randn((rows, heads + 3, d), generator=g, device="cuda") * scale
+        return wide.to(dtype)[:, :heads]
+    return (torch.randn((rows, heads, d), generator=g, device="cuda") * scale).to(dtype)
+
+
+def _cu(new):
+    return [0] + list(itertools.accumulate(new))
+
+
+def _run(q, cache, cu, ctx, window=0, scale=None, attn=None, extra=3):
+    """o and lse of q's rows, with `extra` rows behind the last sequence that must stay as they were."""
+    rows, heads, d = q.shape
+    if extra:
+        q = torch.cat([q, torch.full((extra, heads, d), math.nan, dtype=q.dtype, device="cuda")])
+    o = torch.full((rows + extra, heads, d), SENTINEL, dtype=q.dtype, device="cuda")
+    lse = torch.full((rows + extra, heads), SENTINEL, device="cuda")
+    attn = attn or gdn.PagedAttention(heads, cache.k.shape[2], d, q.dtype, max_batch=len(ctx))
+    attn.run(q, cache.k, cache.v, cache.table, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+             torch.tensor(ctx, dtype=torch.int32, device="cuda"), o, lse, scale=scale, window=window)
+    assert attn.status() == gdn.GDN_OK
+    assert bool((o[rows:] == SENTINEL).all()) and bool((lse[rows:] == SENTINEL).all())
+    return o[:rows], lse[:rows]
+
+
+def _check(q, cache, cu, ctx, o, lse, window=0, scale=None):
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    worst = 0.0
+    for (r0, r1), want, bound, want_lse, lse_bound in ref.attention(q, cache.k, cache.v, cache.table, cu, ctx, scale, window):
+        off = (o[r0:r1].double() - want).abs() / bound
+        assert bool((off <= 1).all()), f"rows {r0}:{r1}: {float(off.nan_to_num(nan=math.inf).max())} of the bound"
+        worst = max(worst, float(off.max()))
+        got = lse[r0:r1].double()
+        none = torch.isinf(want_lse)
+        assert torch.equal(torch.isinf(got) & (got < 0), none)
+        off = torch.where(none, 0.0, (got - want_lse).abs() / lse_bound)
+        assert bool((off <= 1).all()), f"lse of rows {r0}:{r1}: {float(off.nan_to_num(nan=math.inf).max())} of the bound"
+    return worst
+
+
+def _case(dtype, heads, kv, d, page, new, ctx, window=0, scale=None, seed=0, layout="packed", q_scale=1.0, k_scale=1.0,
+          strided=False):
+    cache = ref.Paged(ctx, kv, d, page, dtype, seed, layout, k_scale)
+    q = _queries(new, heads, d, dtype, seed, q_scale, strided)
+    cu = _cu(new)
+    o, lse = _run(q, cache, cu, ctx, window, scale, extra=0 if strided else 3)
+    _check(q, cache, cu, ctx, o, lse, window, scale)
+    return q, cache, cu, o, lse
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv,page", [(8, 8, 16), (16, 2, 64), (6, 2, 48), (7, 1, 8)])
+def test_single_tokens(dtype, d, heads, kv, page):
+    ctx = [1, 2, 15, 16, 17, 127, 128, 129, 0, 255, 257, 1000, 4097]
+    _case(dtype, heads, kv, d, page, [1] * len(ctx), ctx, seed=d + page)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv,page", [(4, 4, 32), (8, 2, 16), (5, 1, 256), (12, 4, 24)])
+def test_chunks(dtype, d, heads, kv, page):
+    new = [1, 5, 16, 0, 17, 33, 64, 100, 129, 300, 0]
+    ctx = [700, 5, 129, 40, 256, 1000, 64, 101, 130, 2000, 0]
+    _case(dtype, heads, kv, d, page, new, ctx, seed=3 * d + page)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window", [1, 2, 7, 64, 128, 200, 5000])
+def test_windows(dtype, window):
+    new = [1, 40, 130, 260, 1]
+    ctx = [900, 333, 130, 1500, 3]
+    _case(dtype, 6, 2, 64, 16, new, ctx, window=window, seed=window)
+    _case(dtype, 2, 2, 128, 64, new, ctx, window=window, seed=window + 1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_pages_before_the_window_are_not_read(dtype):
+    """Page numbers of pages that no row's window reaches are garbage; rows before the window hold NaN."""
+    page, window, ctx, new = 16, 40, [500, 333, 1111], [1, 20, 150]
+    cache = ref.Paged(ctx, 2, 128, page, dtype, 5)
+    q, cu = _queries(new, 4, 128, dtype, 5), _cu(new)
+    want = list(ref.attention(q, cache.k, cache.v, cache.table, cu, ctx, 128 ** -0.5, window))
+    for b, (n, c) in enumerate(zip(new, ctx)):
+        lo = max(0, c - n - window + 1)
+        i = torch.arange(lo, device="cuda")
+        pages = cache.table[b][i // page].long()
+        cache.k[pages, i % page] = math.nan
+        cache.v[pages, i % page] = math.inf
+        cache.table[b, :lo // page] = -5
+    o, lse = _run(q, cache, cu, ctx, window)
+    for (r0, r1), w, bound, _, _ in want:
+        assert bool(((o[r0:r1].double() - w).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_without_keys(dtype):
+    """More new tokens than context: the rows before position 0 see nothing."""
+    new, ctx = [10, 200, 3, 150], [4, 0, 3, 149]
+    q, cache, cu, o, lse = _case(dtype, 4, 2, 128, 16, new, ctx)
+    assert bool((o[:6] == 0).all()) and bool(torch.isinf(lse[:6]).all())
+    assert bool((o[10:210] == 0).all()) and bool(torch.isinf(lse[10:210]).all())
+    assert bool(torch.isfinite(lse[6:10]).all())
+
+
+@pytest.mark.parametrize("dtype,heads,kv", [(BF16, 64, 1), (F32, 64, 1), (BF16, 33, 1), (BF16, 22, 2), (F32, 48, 2)])
+def test_large_groups(dtype, heads, kv):
+    _case(dtype, heads, kv, 64, 16, [1, 7, 40], [300, 77, 200], seed=heads)
+    _case(dtype, heads, kv, 128, 32, [3, 1], [140, 1025], seed=heads + 1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", ["heads first", "pairs"])
+def test_cache_layouts_and_strided_queries(dtype, layout):
+    new, ctx = [1, 50, 9], [400, 333, 9]
+    _case(dtype, 8, 4, 128, 16, new, ctx, layout=layout, strided=True, seed=8)
+    _case(dtype, 8, 4, 64, 40, new, ctx, layout=layout, strided=True, window=100, seed=9)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("q_scale", [0.01, 4.0, 30.0])
+def test_score_ranges(dtype, q_scale):
+    """Flat, peaked and one-hot softmax rows; the maximum keeps growing along the keys."""
+    new, ctx = [1, 130], [1500, 700]
+    cache = ref.Paged(ctx, 2, 128, 64, dtype, 11)
+    for b, c in enumerate(ctx):   # later keys are larger
+        i = torch.arange(c, device="cuda")
+        rows = cache.table[b][i // 64].long(), i % 64
+        cache.k[rows] = (cache.k[rows].float() * (0.05 + 2 * i / c)[:, None, None]).to(dtype)
+    q, cu = _queries(new, 4, 128, dtype, 12, q_scale), _cu(new)
+    o, lse = _run(q, cache, cu, ctx)
+    _check(q, cache, cu, ctx, o, lse)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.02, 1e-8])
+def test_scale(scale):
+    _case(BF16, 4, 2, 64, 16, [1, 40], [200, 300], scale=scale, q_scale=0.2, seed=21)
+    _case(F32, 4, 2, 64, 16, [1, 40], [200, 300], scale=scale, q_scale=0.2, seed=22)
+
+
+@pytest.mark.parametrize("dtype,new,ctx", [
+    (BF16, [1], [40001]), (F32, [1], [20011]), (BF16, [3, 1, 2], [9000, 30000, 129]), (BF16, [520], [8712]),
+    (F32, [65], [5000]), (BF16, [1500], [1500]), (BF16, [1] * 300, list(range(1, 301))),
+])
+def test_long_and_many(dtype, new, ctx):
+    _case(dtype, 8, 2, 128, 64, new, ctx, seed=len(ctx))
+
+
+def test_more_sequences_than_one_scan_block():
+    """The schedule's scan over the sequences takes several rounds."""
+    batch = 2500
+    new = [i % 3 for i in range(batch)]
+    ctx = [(7 * i) % 60 + 2 for i in range(batch)]
+    cache = ref.Paged(ctx, 1, 64, 8, BF16, 31)
+    q, cu = _queries(new, 2, 64, BF16, 31), _cu(new)
+    o, lse = _run(q, cache, cu, ctx)
+    _check(q, cache, cu, ctx, o, lse)
+
+
+def test_reruns_give_the_same_bits():
+    new, ctx = [1, 33, 260], [3000, 900, 2600]
+    cache = ref.Paged(ctx, 2, 128, 16, BF16, 41)
+    q, cu = _queries(new, 8, 128, BF16, 41), _cu(new)
+    attn = gdn.PagedAttention(8, 2, 128, BF16, max_batch=3)
+    first = _run(q, cache, cu, ctx, attn=attn)
+    attn.workspace.fill_(0xFF)   # needs no initialisation
+    again = _run(q, cache, cu, ctx, attn=attn)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_without_lse_and_one_shot():
+    new, ctx = [1, 33], [300, 90]
+    cache = ref.Paged(ctx, 2, 128, 16, BF16, 42)
+    q, cu = _queries(new, 8, 128, BF16, 42), _cu(new)
+    o, lse = _run(q, cache, cu, ctx)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = (q, cache.k, cache.v, cache.table, torch.tensor(cu, **i32), torch.tensor(ctx, **i32))
+    assert torch.equal(gdn.paged_attention(*args), o)
+    o2, lse2 = gdn.paged_attention(*args, with_lse=True)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_beyond_32_bits(dtype):
+    """A pool of more than 2^32 elements: pages at its far end."""
+    page, kv, d = 64, 8, 128
+    per_page = 2 * page * kv * d
+    pages = 2 ** 32 // per_page + 40
+    free, _ = torch.cuda.mem_get_info()
+    need = pages * per_page * (2 if dtype == BF16 else 4)
+    if free < need + 2 ** 31:
+        pytest.skip("not enough free memory")
+    pool = torch.empty((pages, 2, page, kv, d), dtype=dtype, device="cuda")
+    k, v = pool[:, 0], pool[:, 1]
+    ctx, new = [600, 70], [1, 20]
+    cache = ref.Paged(ctx, kv, d, page, dtype, 51)
+    far = pages - 1 - torch.arange(cache.pages, device="cuda")
+    k[far], v[far] = cache.k, cache.v
+    cache.k, cache.v = k, v
+    cache.table = torch.where(cache.table < cache.pages, pages - 1 - cache.table, cache.table)
+    q, cu = _queries(new, 16, d, dtype, 51), _cu(new)
+    o, lse = _run(q, cache, cu, ctx)
+    _check(q, cache, cu, ctx, o, lse)
+
+
+def test_bad_descriptors_are_reported_and_skipped():
+    """A page number outside the pool, a context past the table, offsets that decrease or leave the rows: the status
+    says so, rows of sequences that cannot be placed stay, and the other sequences are right."""
+    new, ctx = [20, 3, 1], [200, 90, 500]
+    cache = ref.Paged(ctx, 2, 128, 16, BF16, 61)
+    q, cu = _queries(new, 4, 128, BF16, 61), _cu(new)
+    good, _ = _run(q, cache, cu, ctx)
+    attn = gdn.PagedAttention(4, 2, 128, BF16, max_batch=3)
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def run(table=cache.table, cu=cu, ctx=ctx):
+        o = torch.full(q.shape, SENTINEL, dtype=BF16, device="cuda")
+        attn.run(q, cache.k, cache.v, table, torch.tensor(cu, **i32), torch.tensor(ctx, **i32), o)
+        return o, attn.status()
+
+    for bad in (-1, cache.pages, 2 ** 31 - 1, -2 ** 31):
+        table = cache.table.clone()
+        table[1, 2] = bad
+        o, status = run(table=table)
+        assert status == gdn.GDN_ERR_MISMATCH
+        assert torch.equal(o[:20], good[:20]) and torch.equal(o[23:], good[23:])
+        assert bool(torch.isfinite(o[20:23]).all())
+    width = cache.table.shape[1] * 16
+    for c in (width + 1, 2 ** 31 - 1, -1):
+        o, status = run(ctx=[200, c, 500])
+        assert status == gdn.GDN_ERR_MISMATCH
+        assert bool((o[20:23] == SENTINEL).all()) and torch.equal(o[:20], good[:20]) and torch.equal(o[23:], good[23:])
+    for offsets in ([0, 20, 23, 25], [0, 20, 23, 2 ** 31 - 1], [0, 20, 10, 24], [-1, 20, 23, 24]):
+        o, status = run(cu=offsets)
+        assert status == gdn.GDN_ERR_MISMATCH
+    o, status = run()
+    assert status == gdn.GDN_OK and torch.equal(o, good)
+
+
+def test_captured_call_follows_new_lengths():
+    """A captured call replayed with other lengths, pages and values gives what an eager call gives."""
+    ctx, new = [900, 60, 333], [1, 4, 20]
+    cache = ref.Paged(ctx, 2, 128, 16, BF16, 71, width=80)
+    q, cu = _queries(new, 8, 128, BF16, 71), _cu(new)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu_t, ctx_t = torch.tensor(cu, **i32), torch.tensor([5, 4, 20], **i32)
+    o = torch.zeros_like(q)
+    attn = gdn.PagedAttention(8, 2, 128, BF16, max_batch=3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        attn.run(q, cache.k, cache.v, cache.table, cu_t, ctx_t, o)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn.run(q, cache.k, cache.v, cache.table, cu_t, ctx_t, o)
+    for lens in ([900, 60, 333], [17, 4, 100], [640, 33, 20]):
+        ctx_t.copy_(torch.tensor(lens, **i32))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager, _ = _run(q, cache, cu, lens, extra=0)
+        assert torch.equal(o, eager)
+
+
+def test_two_calls_at_once():
+    """Two streams with a workspace each, against the same calls one after the other."""
+    ctx, new = [9000, 800], [1, 130]
+    cache = ref.Paged(ctx, 2, 128, 64, BF16, 81)
+    q, cu = _queries(new, 8, 128, BF16, 81), _cu(new)
+    want, _ = _run(q, cache, cu, ctx)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu_t, ctx_t = torch.tensor(cu, **i32), torch.tensor(ctx, **i32)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    attns = [gdn.PagedAttention(8, 2, 128, BF16, max_batch=2) for _ in range(2)]
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, a, o in zip(streams, attns, outs):
+            a.run(q, cache.k, cache.v, cache.table, cu_t, ctx_t, o, stream=s)
+    torch.cuda.synchronize()
+    for a, o in zip(attns, outs):
+        assert a.status() == gdn.GDN_OK and torch.equal(o, want)
