@@ -174,20 +174,9 @@ struct SimtSmem {
     float p[kRows][kKeys + 4];
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-    return *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                       __uint_as_float(x.y & 0xffff0000u));
-}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
     extern __shared__ float smem_raw[];
     SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(smem_raw);
@@ -209,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
             const int r = i / (D / 4), c = (i % (D / 4)) * 4;
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (r < rows)
-                x = load4(static_cast<const T*>(a.q) + (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.rs_q +
+                x = load4(static_cast<const float*>(a.q) + (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.rs_q +
                           (long long)(u.head * a.group + r % a.group) * D + c);
             *reinterpret_cast<float4*>(&sm.q[r][c]) = x;
         }
@@ -233,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 if (key >= u.r.lo && key < u.r.hi) {
                     const int page = a.page_table[(long long)u.b * a.max_pages + key / a.page_size];
                     if (page >= 0 && page < a.num_pages)
-                        x = load4(static_cast<const T*>(base) + (long long)page * a.page_stride +
+                        x = load4(static_cast<const float*>(base) + (long long)page * a.page_stride +
                                   (long long)(key % a.page_size) * a.row_stride + (long long)u.head * a.head_stride + c);
                     else if (c == 0)
                         report(a, kStatusMismatch);
@@ -340,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 for (int j = 0; j < D / 64; ++j) {
                     const float4 x = make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
                                                  o[i][4 * j + 3] * inv);
-                    if (whole) store4(static_cast<T*>(a.o) + orow * D + 4 * tx + 64 * j, x);
+                    if (whole) store4(static_cast<float*>(a.o) + orow * D + 4 * tx + 64 * j, x);
                     else *reinterpret_cast<float4*>(a.part_o + prow * D + 4 * tx + 64 * j) = x;
                 }
                 if (tx == 0) {
@@ -359,30 +348,27 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simt_typed(const Args& a, cudaStream_t stream) {
     static std::atomic<uint64_t> smem_set{0};
     const cudaError_t e =
-        ensure_smem_limit(reinterpret_cast<const void*>(simt_kernel<T, D>), (int)sizeof(SimtSmem<D>), smem_set);
+        ensure_smem_limit(reinterpret_cast<const void*>(simt_kernel<D>), (int)sizeof(SimtSmem<D>), smem_set);
     if (e != cudaSuccess) return e;
-    simt_kernel<T, D><<<a.shape.max_parts, kThreads, sizeof(SimtSmem<D>), stream>>>(a);
+    simt_kernel<D><<<a.shape.max_parts, kThreads, sizeof(SimtSmem<D>), stream>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-Shape shape_simt(int) { return Shape{kRows, 1, kKeys, 296, 2}; }
+constexpr Shape kSimtShape{kRows, 1, kKeys, 296, 2};
 
 cudaError_t launch_simt(const Args& a, cudaStream_t stream) {
-    if (a.dtype == GDN_F32)
-        return a.dim == 64 ? launch_simt_typed<float, 64>(a, stream) : launch_simt_typed<float, 128>(a, stream);
-    return a.dim == 64 ? launch_simt_typed<__nv_bfloat16, 64>(a, stream)
-                       : launch_simt_typed<__nv_bfloat16, 128>(a, stream);
+    return a.dim == 64 ? launch_simt_typed<64>(a, stream) : launch_simt_typed<128>(a, stream);
 }
 
 }  // namespace attn
 
-attn::Shape paged_attention_shape(int, int dim) { return attn::shape_simt(dim); }
+attn::Shape paged_attention_shape(int dtype, int) { return dtype == GDN_F32 ? attn::kSimtShape : attn::shape_tc(); }
 
 attn::Layout paged_attention_layout(int dtype, int dim, int batch) {
     const attn::Shape sh = paged_attention_shape(dtype, dim);
@@ -401,7 +387,7 @@ cudaError_t launch_paged_attention(const attn::Args& a, cudaStream_t stream) {
     attn::line_kernel<<<1, 1024, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = attn::launch_simt(a, stream);
+    e = a.dtype == GDN_F32 ? attn::launch_simt(a, stream) : attn::launch_tc(a, stream);
     if (e != cudaSuccess) return e;
     // rows of a unit, at most those of the call
     const long long unit_rows = (long long)a.shape.subs * a.shape.sub_rows;

@@ -183,8 +183,8 @@ __device__ __forceinline__ long long part_slot(long long part, bool begins_stret
     return 2 * part + (begins_stretch ? 0 : 1);
 }
 
-cudaError_t launch_simt(const Args& a, cudaStream_t stream);
-Shape shape_simt(int dim);
+cudaError_t launch_tc(const Args& a, cudaStream_t stream);   // bf16
+Shape shape_tc();
 
 }  // namespace attn
 

@@ -666,12 +666,9 @@ prefill_pipe_kernel(const TcParams p, const __grid_constant__ CUtensorMap map_k,
     }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
+}  // namespace
 
-EncodeTiledFn encode_fn() {
+EncodeTiledFn tensor_map_encoder() {
     // resolved once (thread-safe static initialisation); null if the driver lacks it
     static const EncodeTiledFn fn = [] {
         void* p = nullptr;
@@ -684,12 +681,10 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-}  // namespace
-
 // [rows][H][128] bf16 with rows row_stride elements apart, box = 64 columns x 1 head
 // x 64 rows, 128-byte swizzle.
 bool make_tile_map(CUtensorMap* m, const void* base, int H, long long rows, long long row_stride) {
-    EncodeTiledFn enc = encode_fn();
+    EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;
     if (rows < 1) rows = 1;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows};

@@ -68,8 +68,8 @@ unsigned int next_call_number();
 // another thread's change, and a word changes at most a few times per call (one
 // retag, then once per status bit), so the loop ends; the cap only bounds it.  Out
 // of line: inlined at every wait site, the loop slowed the prefill kernel by 3%.
-static __device__ __noinline__ void tag_merge(unsigned long long* word, unsigned int epoch, unsigned int val,
-                                          bool first_only) {
+__device__ __forceinline__ void tag_merge_inline(unsigned long long* word, unsigned int epoch, unsigned int val,
+                                                 bool first_only) {
     unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
     for (int i = 0; i < 64; ++i) {
         const unsigned int low = (unsigned int)(old >> 32) == epoch ? (unsigned int)old : 0u;
@@ -80,6 +80,10 @@ static __device__ __noinline__ void tag_merge(unsigned long long* word, unsigned
         if (seen == old) return;
         old = seen;
     }
+}
+static __device__ __noinline__ void tag_merge(unsigned long long* word, unsigned int epoch, unsigned int val,
+                                          bool first_only) {
+    tag_merge_inline(word, epoch, val, first_only);
 }
 
 // Index checks of the debug build (compiled with -DGDN_DEBUG_BOUNDS).  Each
