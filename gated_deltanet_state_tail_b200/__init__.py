@@ -401,123 +401,164 @@ def gdn_workspace_status(workspace, stream=None) -> int:
     return int(_lib.gdn_workspace_status(_ptr(workspace), _stream_handle(stream)))
 
 
-def _rows_of(t, heads, dim, name):
-    """Row stride (elements) of a [rows, heads, dim] view with contiguous heads inside a row."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+# The operators below are called once per layer and token, so their argument checks are
+# written to cost little: no torch import, stream object or library lookup per call.
+
+def _row_stride(t, heads, dim, name):
+    """Row stride (elements; 0 = packed) of a [rows, heads, dim] view with contiguous heads inside a row."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim]")
+    rows, h, d = t.shape
+    if h != heads or d != dim:
         raise ValueError(f"{name} must be [rows, {heads}, {dim}]")
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    s0, s1, s2 = t.stride()
+    if rows and (s2 != 1 or (heads > 1 and s1 != dim)):
         raise ValueError(f"{name} must have contiguous heads inside a row")
-    return t.stride(0) if t.shape[0] > 1 else 0
+    return s0 if rows > 1 else 0
 
 
 def _dense(t, shape, dtype, name):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
 
 
-def _same_device(*tensors):
-    """Every tensor on the current CUDA device, where the call launches."""
-    import torch
-    here = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else None
+def _launch_device(*tensors):
+    """The current CUDA device, where the call launches and every tensor must be."""
+    here = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != here):
-            raise ValueError("every tensor must be on the current CUDA device")
+        if t is not None and t.get_device() != here:
+            here = -1
+    if here < 0 or here != _torch().cuda.current_device():
+        raise ValueError("every tensor must be on the current CUDA device")
+    return here
+
+
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _launch_stream(stream, device):
+    if stream is not None:
+        if stream.device_index != device:
+            raise ValueError("the stream belongs to another device")
+        return stream.cuda_stream
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the current stream without an object around it
+    return raw(device) if raw is not None else torch.cuda.current_stream().cuda_stream
+
+
+_entry = {}
+
+
+def _fn(name):
+    """The library's entry point, looked up once."""
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(library(), name)
+    return f
 
 
 def _paged_kv(k_cache, v_cache):
     """Descriptor of [num_pages, page_size, num_kv_heads, head_dim] key and value pools (any strides with
     contiguous elements inside a head, the same for both)."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape != v_cache.shape or k_cache.dtype is not v_cache.dtype:
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim], alike")
-    if k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+    if stride != v_cache.stride() or stride[3] != 1:
         raise ValueError("k_cache and v_cache must share their strides, with contiguous elements inside a head")
-    c = gdn_paged_kv()
-    c.num_pages, c.page_size, c.num_kv_heads, c.head_dim = k_cache.shape
-    c.dtype = _dtype_code(k_cache.dtype)
-    if not k_cache.is_contiguous():
-        c.page_stride, c.row_stride, c.head_stride = k_cache.stride()[:3]
-    return c
+    pages, page, heads, dim = shape
+    if k_cache.is_contiguous():
+        return gdn_paged_kv(pages, page, heads, dim, _dtype_code(k_cache.dtype), 0, 0, 0, 0)
+    return gdn_paged_kv(pages, page, heads, dim, _dtype_code(k_cache.dtype), 0, *stride[:3])
 
 
 def gdn_qk_norm_rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, k_cache, v_cache, slots, q_out, k_out,
                      interleaved=False, stream=None):
     """Norm, rotation and cache append (see ``qk_norm_rope``); every output is given."""
-    import torch
-    _same_device(q, k, v, positions, inv_freq, q_weight, k_weight, k_cache, v_cache, slots, q_out, k_out)
+    torch = _torch()
+    device = _launch_device(q, k, v, positions, inv_freq, q_weight, k_weight, k_cache, v_cache, slots, q_out, k_out)
     if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise ValueError("q must be [rows, num_heads, head_dim] and k [rows, num_kv_heads, head_dim]")
     rows, heads, dim = q.shape
     kv = k.shape[1]
-    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+    dtype = q.dtype
+    if k.dtype is not dtype or (v is not None and v.dtype is not dtype):
         raise ValueError("q, k and v must have one dtype")
-    d = gdn_qk_desc()
-    d.rows, d.num_heads, d.num_kv_heads, d.head_dim = rows, heads, kv, dim
-    d.rotary_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
-    d.rotary_style = GDN_ROTARY_INTERLEAVED if interleaved else GDN_ROTARY_HALVES
-    d.dtype = _dtype_code(q.dtype)
-    d.q_row_stride, d.k_row_stride = _rows_of(q, heads, dim, "q"), _rows_of(k, kv, dim, "k")
+    rot = 0
     if inv_freq is not None:
-        _dense(inv_freq, (inv_freq.numel(),), torch.float64, "inv_freq")
+        half = inv_freq.numel()
+        rot = 2 * half
+        _dense(inv_freq, (half,), torch.float64, "inv_freq")
         _dense(positions, (rows,), torch.int64, "positions")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _dense(w, (dim,), torch.float32, name)
-    _dense(q_out, (rows, heads, dim), q.dtype, "q_out")
+    if q_weight is not None:
+        _dense(q_weight, (dim,), torch.float32, "q_weight")
+    if k_weight is not None:
+        _dense(k_weight, (dim,), torch.float32, "k_weight")
+    _dense(q_out, (rows, heads, dim), dtype, "q_out")
     if k_out is not None:
-        _dense(k_out, (rows, kv, dim), q.dtype, "k_out")
-    cache = None
+        _dense(k_out, (rows, kv, dim), dtype, "k_out")
+    cache, v_stride, v_ptr, k_pages, v_pages, slot_ptr = None, 0, None, None, None, None
     if k_cache is not None:
         if v is None or v_cache is None or slots is None or v.shape[0] != rows:
             raise ValueError("a cache needs v, v_cache and slots, one row of each per row of k")
-        d.v_row_stride = _rows_of(v, kv, dim, "v")
+        v_stride = _row_stride(v, kv, dim, "v")
         _dense(slots, (rows,), torch.int64, "slots")
-        c = _paged_kv(k_cache, v_cache)
-        if k_cache.dtype != q.dtype:
+        if k_cache.dtype is not dtype:
             raise ValueError("the cache must have the dtype of q, k and v")
-        cache = ctypes.byref(c)
+        cache = ctypes.byref(_paged_kv(k_cache, v_cache))
+        v_ptr, k_pages, v_pages, slot_ptr = v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
     elif slots is not None or v_cache is not None:
         raise ValueError("slots and v_cache need k_cache")
-    _check(_lib.gdn_qk_norm_rope(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v) if cache else None, _ptr(positions),
-                                 _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), eps, cache, _ptr(slots),
-                                 _ptr(k_cache), _ptr(v_cache), _ptr(q_out), _ptr(k_out), _stream_handle(stream)),
-           "gdn_qk_norm_rope")
+    d = gdn_qk_desc(rows, heads, kv, dim, rot, GDN_ROTARY_INTERLEAVED if interleaved else GDN_ROTARY_HALVES,
+                    _dtype_code(dtype), _row_stride(q, heads, dim, "q"), _row_stride(k, kv, dim, "k"), v_stride)
+    _check(_fn("gdn_qk_norm_rope")(
+        ctypes.byref(d), q.data_ptr(), k.data_ptr(), v_ptr, _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
+        _ptr(k_weight), eps, cache, slot_ptr, k_pages, v_pages, q_out.data_ptr(), _ptr(k_out),
+        _launch_stream(stream, device)), "gdn_qk_norm_rope")
 
 
 def gdn_paged_attention_workspace_bytes(dtype, head_dim, max_batch) -> int:
-    return int(_lib.gdn_paged_attention_workspace_bytes(_dtype_code(dtype), int(head_dim), int(max_batch)))
+    return int(_fn("gdn_paged_attention_workspace_bytes")(_dtype_code(dtype), int(head_dim), int(max_batch)))
 
 
 def gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace, scale=None,
                         window=0, stream=None):
     """Causal attention of new tokens over a paged cache (see ``PagedAttention.run``)."""
-    import torch
-    _same_device(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace)
+    torch = _torch()
+    device = _launch_device(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace)
     c = _paged_kv(k_cache, v_cache)
-    if q.dim() != 3 or q.dtype != k_cache.dtype:
+    if q.dim() != 3 or q.dtype is not k_cache.dtype:
         raise ValueError("q must be [rows, num_heads, head_dim] of the cache's dtype")
     rows, heads, dim = q.shape
     if dim != c.head_dim:
         raise ValueError("q and the cache must have one head_dim")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [batch, max_pages]")
-    batch = page_table.shape[0]
-    _dense(page_table, page_table.shape, torch.int32, "page_table")
+    batch, width = page_table.shape
+    _dense(page_table, (batch, width), torch.int32, "page_table")
     _dense(cu_seqlens, (batch + 1,), torch.int32, "cu_seqlens")
     _dense(context_len, (batch,), torch.int32, "context_len")
     _dense(o_out, (rows, heads, dim), q.dtype, "o_out")
     if lse_out is not None:
         _dense(lse_out, (rows, heads), torch.float32, "lse_out")
-    need = _lib.gdn_paged_attention_workspace_bytes(c.dtype, dim, batch)
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    need = _fn("gdn_paged_attention_workspace_bytes")(c.dtype, dim, batch)
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"the workspace must have at least {need} bytes")
-    d = gdn_attn_desc()
-    d.batch, d.num_heads, d.rows, d.q_row_stride = batch, heads, rows, _rows_of(q, heads, dim, "q")
-    d.max_pages, d.window = page_table.shape[1], int(window)
-    d.scale = dim ** -0.5 if scale is None else scale
-    _check(_lib.gdn_paged_attention(ctypes.byref(d), ctypes.byref(c), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                    _ptr(page_table), _ptr(cu_seqlens), _ptr(context_len), _ptr(o_out), _ptr(lse_out),
-                                    _ptr(workspace), _stream_handle(stream)),
-           "gdn_paged_attention")
+    d = gdn_attn_desc(batch, heads, rows, _row_stride(q, heads, dim, "q"), width, int(window),
+                      dim ** -0.5 if scale is None else scale, 0)
+    _check(_fn("gdn_paged_attention")(
+        ctypes.byref(d), ctypes.byref(c), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+        cu_seqlens.data_ptr(), context_len.data_ptr(), o_out.data_ptr(), _ptr(lse_out), workspace.data_ptr(),
+        _launch_stream(stream, device)), "gdn_paged_attention")
 
 
 class _Plan:
@@ -660,9 +701,10 @@ class PagedAttention:
         [B, max_pages], cu_seqlens [B + 1], context_len [B] int32; o_out [rows, H, d] and lse_out [rows, H] fp32
         are written at the rows that sequences own.  Row i of a sequence with n new tokens and context L is
         position L - n + i and sees the keys up to it, with a window only the last `window` of them."""
-        if q.shape[1:] != (self.num_heads, self.head_dim) or k_cache.shape[2] != self.num_kv_heads:
+        rows, heads, dim = q.shape
+        if heads != self.num_heads or dim != self.head_dim or k_cache.shape[2] != self.num_kv_heads:
             raise ValueError("q or the cache has other heads than this PagedAttention")
-        if page_table.shape[0] > self.max_batch or (self.max_rows is not None and q.shape[0] > self.max_rows):
+        if page_table.shape[0] > self.max_batch or (self.max_rows is not None and rows > self.max_rows):
             raise ValueError("more sequences or rows than this PagedAttention was made for")
         gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out,
                             self.workspace if workspace is None else workspace, scale, window, stream)
@@ -694,12 +736,13 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
 
     q, k and v are [rows, heads, d] (row-strided views too).  Returns (q_out, k_out); k_out is made only where
     there is no cache and none was given."""
-    import torch
-    with torch.cuda.stream(stream):   # what is made here is made on the stream that fills it
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k_out is None and k_cache is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if q_out is None or (k_out is None and k_cache is None):
+        torch = _torch()
+        with torch.cuda.stream(stream):   # what is made here is made on the stream that fills it
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if k_out is None and k_cache is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     gdn_qk_norm_rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, k_cache, v_cache, slots, q_out, k_out,
                      interleaved, stream)
     return q_out, k_out

@@ -1,5 +1,5 @@
-// gdn_attn.cu -- attention of a chunk of new tokens over a paged cache: the kernels that
-// lay out and merge the work (gdn_attn.h), and the fp32 attention kernel.
+// gdn_attn.cu -- attention of a chunk of new tokens over a paged cache: the layout of
+// the work for many sequences (gdn_attn.h), and the fp32 attention kernel.
 //
 // Per new token i of a sequence with n new tokens and context L (position p = L - n + i)
 // and query head h, over the keys j in (p - window, p], j >= 0, of key head h / group:
@@ -32,22 +32,9 @@ __global__ void __launch_bounds__(1024) line_kernel(const Args a) {
         a.ws->epoch = a.epoch;
         carry = 0;
     }
-    const long long max_ctx = (long long)a.max_pages * a.page_size;
     for (int b = warp; b < a.batch; b += 32) {
-        const int r0 = a.cu[b], r1 = a.cu[b + 1], ctx = a.ctx[b];
-        const bool good = r0 >= 0 && r1 >= r0 && r1 <= a.rows && ctx >= 0 && ctx <= max_ctx;
-        Seq s;
-        s.row0 = r0;
-        s.qlen = good ? r1 - r0 : 0;
-        s.ctx = ctx;
-        s.pad = 0;
-        long long n = 0;
-        const int blocks = token_blocks(a, s.qlen);
-        for (int t = lane; t < blocks; t += 32) n += block_range(a, s.qlen, ctx, t).tiles;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-        s.head_tiles = n;
-        s.before = 0;
+        bool good;
+        const Seq s = load_seq<true>(a, b, good);
         if (lane == 0) {
             a.seqs[b] = s;
             if (!good) report(a, kStatusMismatch);
@@ -81,127 +68,90 @@ __global__ void __launch_bounds__(1024) line_kernel(const Args a) {
         if (threadIdx.x == 0) carry += warp_sum[31];
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        const long long total = carry;
-        long long per = (total + a.shape.max_parts - 1) / a.shape.max_parts;
-        if (per < a.shape.min_tiles) per = a.shape.min_tiles;
-        a.line->total = total;
-        a.line->per_part = per;
-        a.line->parts = (int)((total + per - 1) / per);
-    }
-}
-
-// --------------------------------------------------------------- the merge
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float4 x);
-template <>
-__device__ __forceinline__ void store4<float>(float* p, float4 x) {
-    *reinterpret_cast<float4*>(p) = x;
-}
-template <>
-__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 x) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-}
-
-// Block (i, y): the unit that the cut before CTA i + 1 is the first to split, rows
-// 8 y .. 8 y + 7, a warp per row.  Weights exp2(lse - max) over the unit's parts, in the
-// order of the line.  Bound by latency: a few hundred KB at most.
-template <typename T>
-__global__ void __launch_bounds__(256) combine_kernel(const Args a) {
-    const long long part = (long long)blockIdx.x + 1;
-    const Line& ln = *a.line;
-    if (part >= ln.parts) return;
-    const long long per = ln.per_part, cut = part * per;
-    const Unit u = find_unit(a, cut);
-    if (u.begin == cut) return;                    // a unit begins here: nothing is split
-    const long long first = u.begin / per, last = (u.begin + u.r.tiles - 1) / per;
-    if (first != part - 1) return;                 // an earlier cut's block merges it
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int unit_rows = a.shape.subs * a.shape.sub_rows;
-    if (row >= unit_rows) return;
-    const int in = row % a.shape.sub_rows;
-    const int tok = (row / a.shape.sub_rows) * a.block_tokens + in / a.group;
-    if (in >= a.block_tokens * a.group || tok >= u.r.toks) return;
-
-    auto slot_row = [&](long long p) {
-        const bool begins = p > first || u.begin == first * per;
-        return part_slot(p, begins) * unit_rows + row;
-    };
-    float top = -INFINITY;
-    for (long long p = first + lane; p <= last; p += 32) top = fmaxf(top, a.part_lse[slot_row(p)]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
-    const bool mine = lane * 4 < a.dim;
-#pragma unroll 4
-    for (long long p = first; p <= last; ++p) {
-        const long long sr = slot_row(p);
-        const float w = exp2f(a.part_lse[sr] - ref);
-        sum += w;
-        if (mine && w > 0.0f) {
-            const float4 x = *reinterpret_cast<const float4*>(a.part_o + sr * a.dim + lane * 4);
-            acc.x = fmaf(w, x.x, acc.x);
-            acc.y = fmaf(w, x.y, acc.y);
-            acc.z = fmaf(w, x.z, acc.z);
-            acc.w = fmaf(w, x.w, acc.w);
-        }
-    }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const long long orow = (long long)(u.s.row0 + u.r.tok0 + tok) * a.num_heads + u.head * a.group + in % a.group;
-    if (mine)
-        store4(static_cast<T*>(a.o) + orow * a.dim + lane * 4,
-               make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    if (a.lse && lane == 0) a.lse[orow] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    if (threadIdx.x == 0) *a.line = make_line(a, carry);
 }
 
 // ------------------------------------------------------------- fp32 attention
 // 64 rows x 64 keys per tile on the CUDA cores.  256 threads: thread (ty, tx) holds the
 // scores of rows 4 ty .. 4 ty + 3 and keys tx + 16 j, and the outputs of those rows and
-// columns 4 tx + 64 j.  K and V of a tile take turns in one shared buffer, so that two
-// CTAs share an SM.  Bound by the fp32 pipe (4 d flops per row and key).
+// columns 4 tx + 64 j.  K of the next tile is copied (cp.async) while P V runs, V while
+// the scores do; 113 KB for d = 128, so that two CTAs share an SM.  Bound by the fp32 pipe
+// (4 d flops per row and key).
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
 
 template <int D>
 struct SimtSmem {
-    static constexpr int LD = D + 4;               // padded row: float4 reads of 8 rows hit 32 banks
-    float q[kRows][LD];
-    float kv[kKeys][LD];
-    float p[kRows][kKeys + 4];
+    float q[kRows][D];
+    float k[kKeys][D + 4];                         // padded: float4 reads of 8 rows hit 32 banks
+    float v[kKeys][D];
+    float p[kRows][kKeys];
 };
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
-    extern __shared__ float smem_raw[];
+    extern __shared__ __align__(16) float smem_raw[];
     SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(smem_raw);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const long long per = a.line->per_part;
-    if ((int)blockIdx.x >= a.line->parts) return;
+    const Line ln = get_line<kThreads>(a, reinterpret_cast<long long*>(smem_raw));
+    if ((int)blockIdx.x >= ln.parts) return;
+    const long long per = ln.per_part;
     long long pos = (long long)blockIdx.x * per;
-    const long long end = min(pos + per, a.line->total);
+    const long long end = min(pos + per, ln.total);
     Unit u = find_unit(a, pos);
     const float scale = a.scale * kLog2e;
     bool begins = true;
-    while (pos < end) {
+    for (;;) {
         const int kt0 = (int)(pos - u.begin);
         const int kt1 = (int)min((long long)u.r.tiles, end - u.begin);
         const int rows = u.r.toks * a.group;
         const int first_pos = u.s.ctx - u.s.qlen + u.r.tok0;
-        // queries
-        for (int i = tid; i < kRows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < rows)
-                x = load4(static_cast<const float*>(a.q) + (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.rs_q +
-                          (long long)(u.head * a.group + r % a.group) * D + c);
-            *reinterpret_cast<float4*>(&sm.q[r][c]) = x;
+        // 64 rows of K or V, zero outside the unit's keys: a warp's lanes share a row
+        // (d = 128) or two, and so a page
+        auto copy_rows = [&](const void* base, float* dst, int ld, int key0) {
+#pragma unroll
+            for (int n = 0; n < kKeys * (D / 4) / kThreads; ++n) {
+                const int i = tid + n * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
+                const int key = key0 + r;
+                const float* src = static_cast<const float*>(base);
+                bool on = key >= u.r.lo && key < u.r.hi;
+                if (on) {
+                    const int page = a.page_table[(long long)u.b * a.max_pages + key / a.page_size];
+                    on = page >= 0 && page < a.num_pages;
+                    if (on)
+                        src += (long long)page * a.page_stride + (long long)(key % a.page_size) * a.row_stride +
+                               (long long)u.head * a.head_stride + c;
+                    else if (c == 0)
+                        report(a, kStatusMismatch);
+                }
+                copy16(dst + r * ld + c, src, on);
+            }
+        };
+        __syncthreads();   // the last unit's reads of shared memory are over
+        // queries and the first tile's keys
+#pragma unroll
+        for (int n = 0; n < kRows * (D / 4) / kThreads; ++n) {
+            const int i = tid + n * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
+            const bool on = r < rows;
+            copy16(&sm.q[r][c],
+                   static_cast<const float*>(a.q) +
+                       (on ? (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.rs_q +
+                                 (long long)(u.head * a.group + r % a.group) * D + c
+                           : 0),
+                   on);
         }
+        copy_rows(a.k, &sm.k[0][0], D + 4, (u.r.tile0 + kt0) * kKeys);
+        copies_commit();
         float m[4], l[4], o[4][D / 16];
         int top_key[4], low_key[4];                // keys [low, top] are seen
 #pragma unroll
@@ -213,28 +163,13 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) o[i][j] = 0.0f;
         }
-        // this tile's K (or V) rows, zero outside the unit's keys
-        auto load_rows = [&](const void* base, int key0) {
-            for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-                const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-                const int key = key0 + r;
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (key >= u.r.lo && key < u.r.hi) {
-                    const int page = a.page_table[(long long)u.b * a.max_pages + key / a.page_size];
-                    if (page >= 0 && page < a.num_pages)
-                        x = load4(static_cast<const float*>(base) + (long long)page * a.page_stride +
-                                  (long long)(key % a.page_size) * a.row_stride + (long long)u.head * a.head_stride + c);
-                    else if (c == 0)
-                        report(a, kStatusMismatch);
-                }
-                *reinterpret_cast<float4*>(&sm.kv[r][c]) = x;
-            }
-        };
         const bool active = (4 * (ty & ~1)) < rows;   // warp-uniform: some row of this warp is a real one
         for (int kt = kt0; kt < kt1; ++kt) {
             const int key0 = (u.r.tile0 + kt) * kKeys;
-            load_rows(a.k, key0);
-            __syncthreads();
+            copy_rows(a.v, &sm.v[0][0], D, key0);     // its last readers passed the barrier below
+            copies_commit();
+            copies_wait<1>();
+            __syncthreads();                          // K (and Q) are in
             float s[4][4];
             if (active) {
 #pragma unroll
@@ -247,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + i][c]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.kv[tx + 16 * j][c]);
+                    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -279,14 +214,16 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                         sum += s[i][j];
                         sm.p[4 * ty + i][tx + 16 * j] = s[i][j];
                     }
-                    l[i] = l[i] * keep + sum;      // this lane's share of the row's sum
+                    l[i] = l[i] * keep + sum;         // this lane's share of the row's sum
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) o[i][j] *= keep;
                 }
             }
-            __syncthreads();                       // K is read, P is written
-            load_rows(a.v, key0);
-            __syncthreads();
+            __syncthreads();                          // K is read
+            if (kt + 1 < kt1) copy_rows(a.k, &sm.k[0][0], D + 4, key0 + kKeys);
+            copies_commit();
+            copies_wait<1>();
+            __syncthreads();                          // V is in, P is written
             if (active) {
 #pragma unroll 2
                 for (int c = 0; c < kKeys; c += 4) {
@@ -297,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int j = 0; j < D / 64; ++j) {
-                            const float4 x = *reinterpret_cast<const float4*>(&sm.kv[c + e][4 * tx + 64 * j]);
+                            const float4 x = *reinterpret_cast<const float4*>(&sm.v[c + e][4 * tx + 64 * j]);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const float p = e == 0 ? pv[i].x : e == 1 ? pv[i].y : e == 2 ? pv[i].z : pv[i].w;
@@ -309,42 +246,88 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                         }
                 }
             }
-            __syncthreads();                       // V and P are read
+            __syncthreads();                          // V and P are read
         }
         const bool whole = kt0 == 0 && kt1 == u.r.tiles;
+        auto out_row = [&](int r) {
+            return (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.num_heads + u.head * a.group + r % a.group;
+        };
         if (active) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float sum = l[i];
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-                const float lse2 = sum > 0.0f ? m[i] + log2f(sum) : -INFINITY;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float lse2 = sum == 0.0f ? -INFINITY : m[i] + log2f(sum);
                 const int r = 4 * ty + i;
                 if (r >= rows) continue;
-                const long long orow = (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.num_heads +
-                                       u.head * a.group + r % a.group;
-                const long long prow = part_slot(blockIdx.x, begins) * kRows + r;
+                const long long orow = out_row(r), prow = part_slot(blockIdx.x, begins) * kRows + r;
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                    const float4 x = make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
-                                                 o[i][4 * j + 3] * inv);
-                    if (whole) store4(static_cast<float*>(a.o) + orow * D + 4 * tx + 64 * j, x);
-                    else *reinterpret_cast<float4*>(a.part_o + prow * D + 4 * tx + 64 * j) = x;
-                }
+                for (int j = 0; j < D / 64; ++j)
+                    *reinterpret_cast<float4*>((whole ? static_cast<float*>(a.o) + orow * D : a.part_o + prow * D) +
+                                               4 * tx + 64 * j) =
+                        make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
+                                    o[i][4 * j + 3] * inv);
                 if (tx == 0) {
-                    if (whole) {
-                        if (a.lse) a.lse[orow] = lse2 * kLn2;
-                    } else {
-                        a.part_lse[prow] = lse2;
+                    if (!whole) a.part_lse[prow] = lse2;
+                    else if (a.lse) a.lse[orow] = lse2 * kLn2;
+                }
+            }
+        }
+        if (!whole) {
+            // the block that brings the unit's last part merges it: eight rows a warp, a row's
+            // columns over its lanes, a few parts of all eight rows read at once
+            __threadfence();
+            const Split sp = split_of(u, per);
+            if (__syncthreads_or(tid == 0 && (claim_arrivals(a, sp, 0), arrive_last(a, sp, 0)))) {
+                const int lane = tid & 31, r0 = (tid >> 5) * 8, n = min(8, rows - r0);
+                RowMerge rm{0.0f, 0.0f, 0.0f};
+                if (lane < n) {
+                    rm = merge_row(a, sp, r0 + lane);
+                    if (a.lse) a.lse[out_row(r0 + lane)] = rm.lse * kLn2;
+                }
+                float4 acc[8];
+                float top[8], inv[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    top[r] = __shfl_sync(0xffffffffu, rm.top, r);
+                    inv[r] = __shfl_sync(0xffffffffu, rm.inv, r);
+                }
+                const int col = 4 * lane;
+#pragma unroll 2
+                for (int p = sp.first; p <= sp.last; ++p) {
+                    const long long base = sp.slot(p) * kRows + r0;
+                    float w[8];
+                    float4 x[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const bool on = r < n && col < D;
+                        w[r] = on ? __ldcg(a.part_lse + base + r) : -INFINITY;
+                        x[r] = on ? __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + r) * D + col))
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float f = exp2f(w[r] - top[r]);
+                        acc[r].x = fmaf(f, x[r].x, acc[r].x);
+                        acc[r].y = fmaf(f, x[r].y, acc[r].y);
+                        acc[r].z = fmaf(f, x[r].z, acc[r].z);
+                        acc[r].w = fmaf(f, x[r].w, acc[r].w);
                     }
                 }
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < n && col < D)
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.o) + out_row(r0 + r) * D + col) =
+                            make_float4(acc[r].x * inv[r], acc[r].y * inv[r], acc[r].z * inv[r], acc[r].w * inv[r]);
             }
         }
         pos = u.begin + kt1;
         begins = false;
-        if (pos < end) next_unit(a, u);
-        __syncthreads();
+        if (pos >= end) break;
+        next_unit(a, u);
     }
 }
 
@@ -360,7 +343,8 @@ cudaError_t launch_simt_typed(const Args& a, cudaStream_t stream) {
 
 }  // namespace
 
-constexpr Shape kSimtShape{kRows, 1, kKeys, 296, 2};
+// two CTAs per SM of a B200
+constexpr Shape kSimtShape{kRows, 1, kKeys, 296, kThreads, 2};
 
 cudaError_t launch_simt(const Args& a, cudaStream_t stream) {
     return a.dim == 64 ? launch_simt_typed<64>(a, stream) : launch_simt_typed<128>(a, stream);
@@ -377,25 +361,25 @@ attn::Layout paged_attention_layout(int dtype, int dim, int batch) {
     attn::Layout l;
     l.line = sizeof(WorkspaceHeader);
     l.seqs = l.line + sizeof(attn::Line);
-    l.part_lse = l.seqs + up(sizeof(attn::Seq) * (size_t)batch);
+    l.arrivals = l.seqs + up(sizeof(attn::Seq) * (size_t)batch);
+    l.part_lse = l.arrivals + up(sizeof(unsigned long long) * (size_t)sh.max_parts * attn::kArrivals);
     l.part_o = l.part_lse + up(sizeof(float) * rows);
     l.bytes = l.part_o + up(sizeof(float) * rows * dim);
     return l;
 }
 
-cudaError_t launch_paged_attention(const attn::Args& a, cudaStream_t stream) {
-    attn::line_kernel<<<1, 1024, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    e = a.dtype == GDN_F32 ? attn::launch_simt(a, stream) : attn::launch_tc(a, stream);
-    if (e != cudaSuccess) return e;
-    // rows of a unit, at most those of the call
-    const long long unit_rows = (long long)a.shape.subs * a.shape.sub_rows;
-    const long long y = a.rows < a.block_tokens ? a.rows * a.group : unit_rows;
-    const dim3 grid((unsigned)(a.shape.max_parts - 1), (unsigned)((y + 7) / 8));
-    if (a.dtype == GDN_F32) attn::combine_kernel<float><<<grid, 256, 0, stream>>>(a);
-    else attn::combine_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_paged_attention(const attn::Args& args, cudaStream_t stream) {
+    attn::Args a = args;
+    // Every CTA lays out the line itself when a thread per sequence suffices and none has
+    // many token blocks to go through (32: under a microsecond); a launch less.
+    const long long step = (long long)a.block_tokens * a.shape.subs;
+    a.line_inline = a.batch <= a.shape.threads && (a.rows + step - 1) / step <= 32;
+    if (!a.line_inline) {
+        attn::line_kernel<<<1, 1024, 0, stream>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return a.dtype == GDN_F32 ? attn::launch_simt(a, stream) : attn::launch_tc(a, stream);
 }
 
 }  // namespace gdn

@@ -7,13 +7,14 @@
 // units' tiles, in the order (sequence, key head, token block), form one line of `total`
 // tiles, and each of `parts` CTAs takes the same length of it, wherever units begin and
 // end.  So one long context with one new token and a thousand short ones both fill the
-// GPU.  A CTA that holds a unit whole writes its outputs; a unit that the cuts split
-// leaves normalised partial outputs and log-sums, merged by the combine kernel in the
-// order of the line: the result does not depend on which CTA ran first.
+// GPU.  A CTA that holds a unit whole writes its outputs.  A unit that the cuts split
+// leaves normalised partial outputs and log-sums; whoever brings the last part of some
+// rows merges all of them, in the order of the line, so the result does not depend on
+// which CTA that was.  (A merging kernel of its own took 10 to 35 us a call.)
 //
-// The lengths are read on the device (a captured call may be replayed with new ones), so
-// a one-block kernel builds the line: per sequence its checked lengths and the tiles
-// before it.
+// The lengths are read on the device (a captured call may be replayed with new ones).
+// When the sequences and their token blocks are few, every CTA lays out the line for
+// itself as it starts; otherwise a one-block kernel does it first.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -23,6 +24,8 @@
 
 namespace gdn {
 namespace attn {
+
+constexpr int kArrivals = 8;     // separately merged shares of a split unit's rows, at most
 
 // One sequence of the line, 32 bytes.
 struct Seq {
@@ -50,6 +53,7 @@ struct Shape {
     int subs;            // row tiles of a unit
     int tile_keys;       // keys of a tile
     int max_parts;       // CTAs of the grid
+    int threads;         // of a CTA
     int min_tiles;       // least tiles of a CTA, so that splitting pays
 };
 
@@ -73,10 +77,12 @@ struct Args {
     float* lse;                             // [rows, num_heads] or null
     WorkspaceHeader* ws;
     unsigned int epoch;
+    int line_inline;                        // every CTA lays out the line itself
     Line* line;
     Seq* seqs;                              // [batch]
+    unsigned long long* arrivals;           // [max_parts * kArrivals]: parts of split units that are in
     float* part_lse;                        // [2 * max_parts][subs * sub_rows], base 2
-    float* part_o;                          // [2 * max_parts][subs * sub_rows][dim]
+    float* part_o;                          // [2 * max_parts] slots of subs * sub_rows * dim values
 };
 
 __device__ __forceinline__ void report(const Args& a, unsigned int bits) {
@@ -177,10 +183,154 @@ __device__ __forceinline__ void next_unit(const Args& a, Unit& u) {
     u.r = block_range(a, u.s.qlen, u.s.ctx, u.t);
 }
 
+// Checks sequence b's entries and counts its tiles, by one thread (WARP = false) or a whole
+// warp.  Entries that do not fit the call's extents give no work: the rows stay as they were.
+template <bool WARP>
+__device__ __forceinline__ Seq load_seq(const Args& a, int b, bool& good) {
+    const int lane = WARP ? threadIdx.x & 31 : 0;
+    const int r0 = a.cu[b], r1 = a.cu[b + 1], ctx = a.ctx[b];
+    good = r0 >= 0 && r1 >= r0 && r1 <= a.rows && ctx >= 0 && ctx <= (long long)a.max_pages * a.page_size;
+    Seq s;
+    s.row0 = r0;
+    s.qlen = good ? r1 - r0 : 0;
+    s.ctx = ctx;
+    s.pad = 0;
+    s.before = 0;
+    long long n = 0;
+    const int blocks = token_blocks(a, s.qlen);
+    for (int t = lane; t < blocks; t += WARP ? 32 : 1) n += block_range(a, s.qlen, ctx, t).tiles;
+    if (WARP) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+    }
+    s.head_tiles = n;
+    return s;
+}
+
+__device__ __forceinline__ Line make_line(const Args& a, long long total) {
+    Line ln;
+    ln.total = total;
+    ln.per_part = max((total + a.shape.max_parts - 1) / a.shape.max_parts, (long long)a.shape.min_tiles);
+    ln.parts = (int)((total + ln.per_part - 1) / ln.per_part);
+    return ln;
+}
+
+// The line as this CTA sees it, by every thread of a block of THREADS; ends with a block
+// barrier.  Laid out here (a thread per sequence: the host saw to it that they suffice),
+// every CTA writes the same values to a.seqs, and reads its own.  `scratch`: one word per
+// warp of shared memory.
+template <int THREADS>
+__device__ __forceinline__ Line get_line(const Args& a, long long* scratch) {
+    if (!a.line_inline) {
+        Line ln = *a.line;
+        __syncthreads();
+        return ln;
+    }
+    const int b = threadIdx.x, warp = b >> 5, lane = b & 31;
+    if (blockIdx.x == 0 && b == 0) a.ws->epoch = a.epoch;
+    Seq s;
+    long long n = 0;
+    if (b < a.batch) {
+        bool good;
+        s = load_seq<false>(a, b, good);
+        if (!good) tag_merge_inline(&a.ws->status, a.epoch, kStatusMismatch, false);
+        n = s.head_tiles * a.num_kv_heads;
+    }
+    long long incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += x;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long before = incl - n, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    if (b < a.batch) {
+        s.before = before;
+        a.seqs[b] = s;
+    }
+    __syncthreads();
+    return make_line(a, total);
+}
+
 // Where a CTA leaves its part of a split unit: two slots per CTA, one for the unit that its
 // stretch of the line begins with and one for the unit that it ends with.
 __device__ __forceinline__ long long part_slot(long long part, bool begins_stretch) {
     return 2 * part + (begins_stretch ? 0 : 1);
+}
+
+// The parts of a split unit: those of CTAs first .. last, in that order.
+struct Split {
+    int first, last;
+    bool from_start;     // the unit begins where CTA first's stretch does
+    __device__ __forceinline__ long long slot(int part) const {
+        return part_slot(part, part > first || from_start);
+    }
+};
+
+__device__ __forceinline__ Split split_of(const Unit& u, long long per) {
+    Split s;
+    s.first = (int)(u.begin / per);
+    s.last = (int)((u.begin + u.r.tiles - 1) / per);
+    s.from_start = u.begin == s.first * per;
+    return s;
+}
+
+// The arrival counts of split units sit in words tagged with the call's number, so that they
+// need no reset before the call.  claim_arrivals: each CTA of a split unit, before its part
+// is counted, gives the word of `share` this call's tag (and the count zero) unless another
+// has; long before the part is done, so that counting it in is a single atomic.
+__device__ __forceinline__ void claim_arrivals(const Args& a, const Split& sp, int share) {
+    unsigned long long* w = a.arrivals + (long long)sp.first * kArrivals + share;
+    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w);
+    while ((unsigned int)(old >> 32) != a.epoch) {   // a retry finds another part's tag: one at most
+        const unsigned long long seen = atomicCAS(w, old, (unsigned long long)a.epoch << 32);
+        if (seen == old) break;
+        old = seen;
+    }
+}
+
+// Counts one more part in, by one thread after its warp's (or block's) threads have written
+// it and fenced; true for the last, which puts the count back to zero for a replay.
+__device__ __forceinline__ bool arrive_last(const Args& a, const Split& sp, int share) {
+    unsigned long long* w = a.arrivals + (long long)sp.first * kArrivals + share;
+    const unsigned int before = (unsigned int)atomicAdd(w, 1ull);
+    if (before != (unsigned int)(sp.last - sp.first)) return false;
+    *reinterpret_cast<volatile unsigned long long*>(w) = (unsigned long long)a.epoch << 32;
+    __threadfence();
+    return true;
+}
+
+// A split unit's row merged: every part has the weight exp2(lse - top) inv.
+struct RowMerge {
+    float top, inv, lse;   // base 2
+};
+__device__ __forceinline__ RowMerge merge_row(const Args& a, const Split& sp, int lse_row) {
+    constexpr int AHEAD = 16;   // parts read at once: the latency of a read is most of the cost
+    const int unit_rows = a.shape.subs * a.shape.sub_rows;
+    float top = -INFINITY, sum = 0.0f;
+    for (int p0 = sp.first; p0 <= sp.last; p0 += AHEAD) {
+        float x[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            x[i] = p0 + i <= sp.last ? __ldcg(a.part_lse + sp.slot(p0 + i) * unit_rows + lse_row) : -INFINITY;
+        float t = top;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) t = fmaxf(t, x[i]);
+        const float ref = t == -INFINITY ? 0.0f : t;
+        sum *= exp2f(top - ref);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) sum += exp2f(x[i] - ref);
+        top = t;
+    }
+    const bool none = sum == 0.0f;   // a NaN part makes the sum, and so the row, NaN
+    const float ref = top == -INFINITY ? 0.0f : top;
+    return RowMerge{ref, none ? 0.0f : 1.0f / sum, none ? -INFINITY : ref + log2f(sum)};
 }
 
 cudaError_t launch_tc(const Args& a, cudaStream_t stream);   // bf16
@@ -191,7 +341,7 @@ Shape shape_tc();
 // Byte offsets of a call's workspace: status header, line, sequences, partial results.
 namespace attn {
 struct Layout {
-    size_t line, seqs, part_lse, part_o, bytes;
+    size_t line, seqs, arrivals, part_lse, part_o, bytes;
 };
 }  // namespace attn
 

@@ -46,6 +46,8 @@ constexpr int kMaxParts = 148;     // one CTA per SM of a B200
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a row's maximum that P absorbs
+constexpr int kPoly = 4;           // of 16 pairs of exponentials, those on the FMA pipe (measured: 0 .. 8)
+constexpr int kMerge = 4;          // parts of a split unit read at once
 constexpr int kBlock = kKeys * 128;   // bytes of one 64-column block of a 128-row tile
 
 template <int D>
@@ -56,7 +58,8 @@ struct Smem {
     static constexpr int KV = 2 * TILE;
     static constexpr int EXCH = KV + STAGES * TILE;           // the streams' maxima and sums: float [2][2][128]
     static constexpr int BARS = EXCH + 2048;
-    static constexpr int BYTES = BARS + 512;
+    static constexpr int SCAN = BARS + 512;                   // the line's scan: a word per warp
+    static constexpr int BYTES = SCAN + 8 * (kThreads / 32);
 };
 
 // This CTA's part of a unit, handed by the walker to the other roles.
@@ -69,7 +72,7 @@ struct Piece {
     int key0;              // first key of the first tile
     int single;            // one row tile: the streams share it
     int slot;              // where partial results go; -1 = the unit is whole here
-    int pad;
+    Split split;           // its parts, if it is not
 };
 
 struct Bars {
@@ -117,13 +120,97 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return r;
 }
 
+// Two fp32 values in one 64-bit register: sm_100 adds and multiplies such pairs in one
+// instruction.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 unpair(Pair p) {
+    float2 x;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(p));
+    return x;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
+    return p;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair p;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+
+// The largest of three, NaN if one is: a NaN score makes its row NaN whichever way its
+// exponentials are computed.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// 2^y of both halves on the FMA pipe, for y in [-127, 128) (below: about 2^-127).  y = n + f
+// with n the nearest integer (found by adding 1.5 * 2^23, whose low bits then hold it), 2^f a
+// polynomial of degree 5 with the least relative error on [-1/2, 1/2] (a Remez fit of its
+// own: 7.5e-8, as fp32 arithmetic 2.4e-7), n added to its exponent.
+__device__ __forceinline__ float2 ex2_poly(Pair y) {
+    const float2 in = unpair(y);
+    y = pair(fmaxf(in.x, -127.0f), fmaxf(in.y, -127.0f));
+    const Pair t = add2(y, pair(12582912.0f, 12582912.0f));
+    const Pair n = add2(t, pair(-12582912.0f, -12582912.0f));
+    const Pair f = fma2(n, pair(-1.0f, -1.0f), y);
+    Pair p = pair(0.0013276472454890609f, 0.0013276472454890609f);
+    p = fma2(p, f, pair(0.009675540961325169f, 0.009675540961325169f));
+    p = fma2(p, f, pair(0.05550713092088699f, 0.05550713092088699f));
+    p = fma2(p, f, pair(0.24022120237350464f, 0.24022120237350464f));
+    p = fma2(p, f, pair(0.6931469440460205f, 0.6931469440460205f));
+    p = fma2(p, f, pair(1.0000001192092896f, 1.0000001192092896f));
+    const float2 e = unpair(p), k = unpair(t);
+    return make_float2(__uint_as_float(__float_as_uint(e.x) + (__float_as_uint(k.x) << 23)),
+                       __uint_as_float(__float_as_uint(e.y) + (__float_as_uint(k.y) << 23)));
+}
+
+// One row's P from its 128 scores: 2^(s scale - m scale) as bf16 into TMEM, their sum
+// returned.  Of 16 pairs, POLY go through the polynomial: the special function unit alone
+// (16 results a clock and SM) would need 2048 clocks for both streams' tiles, as long as the
+// tensor core for d = 128.  (POLY = 0 on tiles with masked keys, whose P must be 0 exactly.)
+template <int POLY>
+__device__ __forceinline__ float probabilities(const float* x, float scale, float off, uint32_t to) {
+    const Pair sc = pair(scale, scale), of = pair(off, off);
+    Pair sum[2] = {0ull, 0ull};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const Pair y = fma2(pair(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), sc, of);
+            float2 e;
+            if ((i * POLY) % 16 < POLY && POLY > 0) {
+                e = ex2_poly(y);
+            } else {
+                e = unpair(y);
+                e.x = ex2(e.x);
+                e.y = ex2(e.y);
+            }
+            sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
+            p[i] = pack(e.x, e.y);
+        }
+        tmem_st16(to + c * 16, p);
+    }
+    const float2 a = unpair(add2(sum[0], sum[1]));
+    return a.x + a.y;
+}
+
 // ------------------------------------------------------------------- walker
 // Walks this CTA's stretch of the line and hands out its pieces, two ahead.
-__device__ __forceinline__ void walk_role(const Args& a, Bars* b) {
+__device__ __forceinline__ void walk_role(const Args& a, const Line& ln, Bars* b) {
     const int lane = threadIdx.x & 31;
-    const long long per = a.line->per_part;
+    const long long per = ln.per_part;
     long long pos = (long long)blockIdx.x * per;
-    const long long end = min(pos + per, a.line->total);
+    const long long end = min(pos + per, ln.total);
     Unit u = find_unit(a, pos);
     for (unsigned i = 0;; ++i) {
         if (i >= 2 && !wait(b, &b->piece_free[i & 1], (i / 2 - 1) & 1)) return;
@@ -142,6 +229,9 @@ __device__ __forceinline__ void walk_role(const Args& a, Bars* b) {
             p.key0 = (u.r.tile0 + kt0) * kKeys;
             p.single = u.r.toks <= a.block_tokens;
             p.slot = p.n == u.r.tiles ? -1 : (int)part_slot(blockIdx.x, i == 0);
+            p.split = split_of(u, per);
+            if (p.slot >= 0 && lane < kArrivals) claim_arrivals(a, p.split, lane);
+            __syncwarp();
             pos += p.n;
         }
         if (lane == 0) {
@@ -192,16 +282,23 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
                         u.row0 + sub * a.block_tokens);
         }
         ++units;
-        for (int j = 0; ok && j < u.n; ++j) {
-            // this lane's run of rows and its page: past the pool (read as zeros) when the
-            // run holds no key of the unit, or the page number is bad
-            const int run = lane % runs;
+        // this lane's run of rows of a tile and its page number, read a tile ahead: past the
+        // pool (read as zeros) when the run holds no key of the unit
+        const int run = lane % runs;
+        auto page_of = [&](int j) {
             const int key = u.key0 + j * kKeys + run * granule;
-            int page = a.num_pages;
-            if (key < u.hi && key + granule > u.lo) {
-                const int p = a.page_table[(long long)u.b * a.max_pages + key / a.page_size];
-                if (p >= 0 && p < a.num_pages) page = p;
-                else *reinterpret_cast<volatile int*>(&b->bad_page) = 1;
+            return j < u.n && key < u.hi && key + granule > u.lo
+                       ? a.page_table[(long long)u.b * a.max_pages + key / a.page_size]
+                       : a.num_pages;
+        };
+        int next_page = page_of(0);
+        for (int j = 0; ok && j < u.n; ++j) {
+            const int key = u.key0 + j * kKeys + run * granule;
+            int page = next_page;
+            next_page = page_of(j + 1);
+            if (page < 0 || page >= a.num_pages) {   // a bad number reads as zeros too, and is reported
+                if (key < u.hi && key + granule > u.lo) *reinterpret_cast<volatile int*>(&b->bad_page) = 1;
+                page = a.num_pages;
             }
             const int in_page = key % a.page_size;
 #pragma unroll
@@ -410,21 +507,22 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + c * 32, x + c * 32);
                 tmem_wait_ld();
-                if (key0 < all_lo || key0 + kKeys - 1 > all_hi) {
+                const bool masked = key0 < all_lo || key0 + kKeys - 1 > all_hi;
+                if (masked) {
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         x[i] = key0 + i >= low_key && key0 + i <= top_key ? x[i] : -INFINITY;
                 }
-                float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
+                float t0 = max3(m, x[0], x[1]), t1 = max3(x[2], x[3], x[4]), t2 = max3(x[5], x[6], x[7]);
 #pragma unroll
-                for (int i = 4; i < 128; i += 4) {
-                    t0 = fmaxf(t0, x[i]);
-                    t1 = fmaxf(t1, x[i + 1]);
-                    t2 = fmaxf(t2, x[i + 2]);
-                    t3 = fmaxf(t3, x[i + 3]);
+                for (int i = 8; i < 128; i += 6) {
+                    t0 = max3(t0, x[i], x[i + 1]);
+                    t1 = max3(t1, x[i + 2], x[i + 3]);
+                    t2 = max3(t2, x[i + 4], x[i + 5]);
                 }
-                const float top = fmaxf(m, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)));
-                if (__any_sync(0xffffffffu, (top - m) * sl > kLazy)) {
+                const float top = max3(t0, t1, t2);
+                // (also when a NaN came in; not when all is still masked)
+                if (__any_sync(0xffffffffu, !((top - m) * sl <= kLazy) && top != -INFINITY)) {
                     const float f = m == -INFINITY ? 0.0f : ex2((m - top) * sl);
                     l *= f;
                     m = top;
@@ -441,24 +539,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                     }
                 }
                 const float off = m == -INFINITY ? 0.0f : -m * sl;
-                float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float e0 = ex2(fmaf(x[32 * c + 2 * i], sl, off)), e1 = ex2(fmaf(x[32 * c + 2 * i + 1], sl, off));
-                        const float e2 = ex2(fmaf(x[32 * c + 2 * i + 2], sl, off)), e3 = ex2(fmaf(x[32 * c + 2 * i + 3], sl, off));
-                        l0 += e0;
-                        l1 += e1;
-                        l2 += e2;
-                        l3 += e3;
-                        p[i] = pack(e0, e1);
-                        p[i + 1] = pack(e2, e3);
-                    }
-                    tmem_st16(tm_s + c * 16, p);
-                }
-                l += (l0 + l1) + (l2 + l3);
+                l += masked ? probabilities<0>(x, sl, off, tm_s) : probabilities<kPoly>(x, sl, off, tm_s);
                 tmem_wait_st();
             }
             any_tile = true;
@@ -480,8 +561,13 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         const int h = row % a.group;
         const long long orow =
             (long long)(u.row0 + sub * a.block_tokens + row / a.group) * a.num_heads + u.head * a.group + h;
-        const long long prow = (long long)u.slot * (2 * kRows) + sub * kRows + row;
         const bool whole = u.slot < 0;
+        // Partial outputs of this warp's rows (single: of this group's half of their columns):
+        // [columns / 4][R] float4 with R the rows of the warp, rounded up to a power of two, so
+        // that both the writes (a lane per row) and the merge's reads are of whole lines.
+        const int warp_rows = min(32, rows - quarter * 32);
+        const int log_r = warp_rows <= 1 ? 0 : 32 - __clz(warp_rows - 1), R = 1 << log_r;
+        const long long warp_at = (long long)(s * 4 + quarter) * 32 * (u.single ? D / 2 : D);   // in a slot
         if (active) {
             // weights of the two streams' sums (the other stream has other rows: 0)
             float f0 = 1.0f, f1 = 0.0f, sum = l, top = m;
@@ -494,7 +580,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                 sum = l0 * f0 + l1 * f1;
                 both = u.n > 1;          // the second stream had a tile
             }
-            const float inv = sum > 0.0f || isnan(sum) ? 1.0f / sum : 0.0f;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             f0 *= inv;
             f1 *= inv;
             // single: this group takes half of the columns, of both streams
@@ -521,17 +607,75 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                             to[i] = make_uint4(pack(o[8 * i], o[8 * i + 1]), pack(o[8 * i + 2], o[8 * i + 3]),
                                                pack(o[8 * i + 4], o[8 * i + 5]), pack(o[8 * i + 6], o[8 * i + 7]));
                     } else {
-                        float4* to = reinterpret_cast<float4*>(a.part_o + prow * D + c * 32);
+                        float4* to = reinterpret_cast<float4*>(a.part_o + (long long)u.slot * (2 * kRows * D) + warp_at) +
+                                     (c - c0) * 8 * R + lane;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            to[i * R] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
             }
-            if (row < rows && (!u.single || s == 0)) {
-                const float lse2 = sum > 0.0f || isnan(sum) ? top * sl + log2f(sum) : -INFINITY;
-                if (!whole) a.part_lse[prow] = lse2;
-                else if (a.lse) a.lse[orow] = lse2 * kLn2;
+            if (row < rows) {
+                const float lse2 = sum == 0.0f ? -INFINITY : top * sl + log2f(sum);
+                // each group keeps a copy with its share of the outputs
+                if (!whole) a.part_lse[(long long)u.slot * (2 * kRows) + s * kRows + row] = lse2;
+                else if (a.lse && (!u.single || s == 0)) a.lse[orow] = lse2 * kLn2;
+            }
+            if (!whole) {
+                // the warp that brings the last part of its rows (single: of its half of their
+                // columns) merges them: lane -> row lane % R and columns 4 (lane / R), 4 (lane / R
+                // + 32 / R), ...; kMerge reads of each of four column groups at once
+                __threadfence();
+                __syncwarp();
+                const bool last = __shfl_sync(0xffffffffu, lane == 0 && arrive_last(a, u.split, s * 4 + quarter), 0);
+                if (last) {
+                    const int r = lane & (R - 1), at = quarter * 32 + r;
+                    const bool mine = at < rows;
+                    RowMerge rm{0.0f, 0.0f, 0.0f};
+                    if (mine) rm = merge_row(a, u.split, s * kRows + at);
+                    const long long to = ((long long)(u.row0 + sub * a.block_tokens + at / a.group) * a.num_heads +
+                                          u.head * a.group + at % a.group) * D + (u.single ? s * (D / 2) : 0);
+                    if (a.lse && mine && lane < R && (!u.single || s == 0)) a.lse[to / D] = rm.lse * kLn2;
+                    const int groups = (u.single ? D / 2 : D) / 4, step = 32 >> log_r;
+                    for (int g0 = lane >> log_r; g0 < groups; g0 += 4 * step) {
+                        float4 acc[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) acc[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int p0 = u.split.first; p0 <= u.split.last; p0 += kMerge) {
+                            float w[kMerge];
+                            float4 y[kMerge][4];
+#pragma unroll
+                            for (int i = 0; i < kMerge; ++i) {
+                                const bool on = mine && p0 + i <= u.split.last;
+                                const long long slot = on ? u.split.slot(p0 + i) : 0;
+                                w[i] = on ? __ldcg(a.part_lse + slot * (2 * kRows) + s * kRows + at) : -INFINITY;
+                                const float4* from =
+                                    reinterpret_cast<const float4*>(a.part_o + slot * (2 * kRows * D) + warp_at) + r;
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    y[i][g] = on && g0 + g * step < groups ? __ldcg(from + (g0 + g * step) * R)
+                                                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            }
+#pragma unroll
+                            for (int i = 0; i < kMerge; ++i) {
+                                const float f = ex2(w[i] - rm.top);
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) {
+                                    acc[g].x = fmaf(f, y[i][g].x, acc[g].x);
+                                    acc[g].y = fmaf(f, y[i][g].y, acc[g].y);
+                                    acc[g].z = fmaf(f, y[i][g].z, acc[g].z);
+                                    acc[g].w = fmaf(f, y[i][g].w, acc[g].w);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if (mine && g0 + g * step < groups)
+                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + to + 4 * (g0 + g * step)) =
+                                    make_uint2(pack(acc[g].x * rm.inv, acc[g].y * rm.inv),
+                                               pack(acc[g].z * rm.inv, acc[g].w * rm.inv));
+                    }
+                }
             }
         }
         // both groups have read both streams' sums and outputs before either stream goes on
@@ -552,7 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars* b = reinterpret_cast<Bars*>(smem + S::BARS);
     const int warp = threadIdx.x >> 5;
-    if ((int)blockIdx.x >= a.line->parts) return;
+    const Line ln = get_line<kThreads>(a, reinterpret_cast<long long*>(smem + S::SCAN));
+    if ((int)blockIdx.x >= ln.parts) return;
     if (smem_u32(smem) & 1023u) {   // the swizzled tiles need it; the runtime places the block's memory so
         if (threadIdx.x == 0) tag_merge_inline(&a.ws->status, a.epoch, kStatusBounds, false);
         return;
@@ -596,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) mma_role<D>(a, smem, b);
         else if (warp == 9) load_role<D>(a, maps, smem, b, granule);
-        else if (warp == 10) walk_role(a, b);
+        else if (warp == 10) walk_role(a, ln, b);
     }
     tc_fence_before();
     __syncthreads();
@@ -629,7 +774,7 @@ cudaError_t launch_typed(const Args& a, const Maps& maps, int granule, cudaStrea
 
 }  // namespace
 
-Shape shape_tc() { return Shape{kRows, 2, kKeys, kMaxParts, 2}; }
+Shape shape_tc() { return Shape{kRows, 2, kKeys, kMaxParts, kThreads, 2}; }
 
 cudaError_t launch_tc(const Args& a, cudaStream_t stream) {
     // rows of one page that a tile's box can hold: the largest power of two that divides the
