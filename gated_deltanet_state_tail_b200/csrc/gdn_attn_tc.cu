@@ -2,16 +2,22 @@
 // (tcgen05 + TMA); the formulas are in gdn_attn.cu, the division of the work in gdn_attn.h.
 //
 // One persistent CTA per SM walks its stretch of the line of key tiles (128 keys).  Ten
-// warps work: a loader, an MMA issuer and two groups of four softmax warps.
+// warps work: a loader, two MMA issuers, a walker along the line and two groups of four
+// softmax warps.
 //   - A row tile holds 128 / group tokens, each with the query heads of one key head, so
 //     shared key heads fill the 128 rows of an MMA with few tokens.
 //   - Two streams share the tensor core: while one stream's softmax runs, the other's
-//     products do.  A unit of more tokens than a row tile gives each stream a row tile and
-//     every key tile serves both; a smaller one (single tokens) has both streams on the
-//     same rows, the even and the odd key tiles, merged at its end.
-//   - Per stream and key tile: S = Q K^T into 128 TMEM columns; one thread per row reads its
-//     128 scores, updates the row's maximum and sum in fp32 and writes P = 2^(S - m) as bf16
-//     over them; O += P V with P read from TMEM, V from shared memory as the cache has it.
+//     products do.  A unit of more tokens than a row tile gives each stream a row tile, and
+//     its steps are the halves (64 keys) of each key tile; a smaller one (single tokens) has
+//     both streams on the same rows, a half of each key tile each, merged at its end.
+//   - Per stream and step: S = Q K^T into 64 TMEM columns, one of two buffers, so that the
+//     next step's scores are there when a softmax ends; one thread per row reads its 64
+//     scores, updates the row's maximum and sum in fp32 and writes P = 2^(S - m) as bf16 over
+//     them; O += P V with P read from TMEM, V from shared memory as the cache has it.  An MMA
+//     of 64 columns with both operands in shared memory takes 48 clocks instead of 32 (a
+//     probe: shared memory feeds it 128 bytes a clock), so a pair of row tiles costs 2480
+//     tensor core clocks per 128 keys instead of 2048; but steps of 128 keys leave no TMEM for
+//     a second buffer, and the chain softmax -> products -> softmax took 3460.
 //   - The maximum that scales P lags: O and the sum are rescaled only when a row's maximum
 //     grew by more than 2^8 since (P up to 256 costs bf16 and fp32 nothing), so the pass
 //     over O is rare after the first tiles.
@@ -38,10 +44,8 @@ using namespace sm100;
 
 constexpr int kRows = 128;         // rows of a row tile
 constexpr int kKeys = 128;         // keys of a tile
-constexpr int kThreads = 384;      // softmax groups: warps 0-3 and 4-7; MMA: 8; loader: 9; walker: 10
-// registers per thread: 168 at launch (65536 / 384, in steps of 8), then the softmax warps
-// take what the third warpgroup gives back: 2 * 208 + 88 = 3 * 168
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kStep = 64;          // keys of a softmax step
+constexpr int kThreads = 384;      // softmax groups: warps 0-3 and 4-7; MMA: 8 and 9; loader: 10; walker: 11
 constexpr int kMaxParts = 148;     // one CTA per SM of a B200
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -58,7 +62,7 @@ struct Smem {
     static constexpr int KV = 2 * TILE;
     static constexpr int EXCH = KV + STAGES * TILE;           // the streams' maxima and sums: float [2][2][128]
     static constexpr int BARS = EXCH + 2048;
-    static constexpr int SCAN = BARS + 512;                   // the line's scan: a word per warp
+    static constexpr int SCAN = BARS + 640;                   // the line's scan: a word per warp
     static constexpr int BYTES = SCAN + 8 * (kThreads / 32);
 };
 
@@ -73,27 +77,31 @@ struct Piece {
     int single;            // one row tile: the streams share it
     int slot;              // where partial results go; -1 = the unit is whole here
     Split split;           // its parts, if it is not
+    // the rows [from, to) of tile j that are keys of the unit
+    __device__ __forceinline__ int from(int j) const { return max(0, lo - (key0 + j * kKeys)); }
+    __device__ __forceinline__ int to(int j) const { return min(kKeys, hi - (key0 + j * kKeys)); }
+    __device__ __forceinline__ bool ragged(int j) const { return from(j) > 0 || to(j) < kKeys; }
 };
 
 struct Bars {
-    uint64_t q_full, q_free, drain, x_full, x_free;
-    uint64_t s_full[2], p_ready[2], o_done[2];
+    uint64_t q_full, q_free, x_full, x_free, drain[2];
+    uint64_t s_full[4], p_ready[4], o_step[4];   // per stream and buffer: 2 s + buffer
     uint64_t piece_full[2], piece_free[2];
     uint64_t kv_full[10], kv_free[10];
+    uint64_t v_raw[10], v_clean[10];   // V tiles with rows outside the unit's keys: loaded, then zeroed there
     Piece piece[2];
     uint32_t tmem;
     int abort;             // a wait ran out
     int bad_page;
 };
-static_assert(sizeof(Bars) <= 512, "the barriers fit their space");
+static_assert(sizeof(Bars) <= 640, "the barriers fit their space");
 
 struct Maps {
     CUtensorMap q, k, v;
 };
 
-// A whole warp's wait, which ends: false (in every lane) when it ran out or another role
-// gave up.
-__device__ __forceinline__ bool wait(Bars* b, uint64_t* bar, uint32_t parity) {
+// A wait that ends, by one thread: false when it ran out or another role gave up.
+__device__ __forceinline__ bool wait_one(Bars* b, uint64_t* bar, uint32_t parity) {
     bool done = mbar_try_wait(bar, parity);
     if (!done) {
         const uint64_t t0 = global_timer_ns();
@@ -105,7 +113,12 @@ __device__ __forceinline__ bool wait(Bars* b, uint64_t* bar, uint32_t parity) {
             }
         }
     }
-    return __all_sync(0xffffffffu, done);
+    return done;
+}
+
+// The same by a whole warp, every lane with the same answer.
+__device__ __forceinline__ bool wait(Bars* b, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_one(b, bar, parity));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -173,16 +186,15 @@ __device__ __forceinline__ float2 ex2_poly(Pair y) {
                        __uint_as_float(__float_as_uint(e.y) + (__float_as_uint(k.y) << 23)));
 }
 
-// One row's P from its 128 scores: 2^(s scale - m scale) as bf16 into TMEM, their sum
+// One row's P from its 64 scores of a step: 2^(s scale - m scale) as bf16 into TMEM, their sum
 // returned.  Of 16 pairs, POLY go through the polynomial: the special function unit alone
-// (16 results a clock and SM) would need 2048 clocks for both streams' tiles, as long as the
-// tensor core for d = 128.  (POLY = 0 on tiles with masked keys, whose P must be 0 exactly.)
+// (16 results a clock and SM) would need 2048 clocks per 128 keys of both streams.  (POLY = 0 on tiles with masked keys, whose P must be 0 exactly.)
 template <int POLY>
 __device__ __forceinline__ float probabilities(const float* x, float scale, float off, uint32_t to) {
     const Pair sc = pair(scale, scale), of = pair(off, off);
     Pair sum[2] = {0ull, 0ull};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2; ++c) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -205,13 +217,21 @@ __device__ __forceinline__ float probabilities(const float* x, float scale, floa
 }
 
 // ------------------------------------------------------------------- walker
-// Walks this CTA's stretch of the line and hands out its pieces, two ahead.
-__device__ __forceinline__ void walk_role(const Args& a, const Line& ln, Bars* b) {
+// Walks this CTA's stretch of the line and hands out its pieces, one ahead of the one in
+// work, whose tiles with rows outside the unit's keys it tends: their V rows there become
+// zero before the MMA warps use the tile.
+template <int D>
+__device__ __forceinline__ void walk_role(const Args& a, const Line& ln, uint8_t* smem, Bars* b) {
+    using S = Smem<D>;
     const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_u32(smem);
     const long long per = ln.per_part;
     long long pos = (long long)blockIdx.x * per;
     const long long end = min(pos + per, ln.total);
     Unit u = find_unit(a, pos);
+    unsigned tiles = 0, tended = 0;   // before the piece being tended; parities of v_raw
+    Piece last;
+    last.n = 0;
     for (unsigned i = 0;; ++i) {
         if (i >= 2 && !wait(b, &b->piece_free[i & 1], (i / 2 - 1) & 1)) return;
         Piece p;
@@ -239,6 +259,25 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, Bars* b
             mbar_arrive(&b->piece_full[i & 1]);
         }
         __syncwarp();
+        for (int j = 0; j < last.n; ++j, ++tiles) {
+            if (!last.ragged(j)) continue;
+            const int from = last.from(j), to = last.to(j);
+            const unsigned st = (2 * tiles + 1) % S::STAGES;
+            if (!wait(b, &b->v_raw[st], (tended >> st) & 1)) return;
+            tended ^= 1u << st;
+            const uint32_t tile = base + S::KV + st * S::TILE;
+            for (int r = lane; r < kKeys * (D / 64); r += 32) {
+                if (r % kKeys >= from && r % kKeys < to) continue;
+                const uint32_t row = tile + (r / kKeys) * kBlock + (r % kKeys) * 128;
+#pragma unroll
+                for (int c = 0; c < 128; c += 16)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + c), "r"(0) : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b->v_clean[st]);
+        }
+        last = p;
         if (p.n == 0) return;
         if (pos < end) next_unit(a, u);
     }
@@ -256,6 +295,14 @@ struct Pieces {
         ++i;
         return p;
     }
+    __device__ __forceinline__ Piece get_one(Bars* b) {   // for a single thread
+        Piece p;
+        p.n = 0;
+        if (wait_one(b, &b->piece_full[i & 1], (i / 2) & 1)) p = b->piece[i & 1];
+        mbar_arrive(&b->piece_free[i & 1]);
+        ++i;
+        return p;
+    }
 };
 
 // ------------------------------------------------------------------- loader
@@ -265,7 +312,7 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
     const int lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
     const int runs = kKeys / granule;           // TMA boxes of one 64-column block
-    unsigned ring = 0, units = 0;
+    unsigned ring = 0, units = 0, raws = 0, raw_any = 0;   // raws: parities of v_raw
     bool ok = true;
     Pieces pieces;
     for (Piece u = pieces.get(b); u.n > 0; u = pieces.get(b)) {
@@ -306,13 +353,20 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
                 const unsigned st = ring % S::STAGES, ph = ring / S::STAGES;
                 ok = ph == 0 || wait(b, &b->kv_free[st], (ph - 1) & 1);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&b->kv_full[st], S::TILE);
+                // a ragged V tile goes to the walker first; its own phase then passes empty
+                const bool raw = kv == 1 && u.ragged(j);
+                uint64_t* full = raw ? &b->v_raw[st] : &b->kv_full[st];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full, S::TILE);
+                    if (raw) mbar_arrive(&b->kv_full[st]);
+                }
+                if (raw) raws ^= 1u << st, raw_any |= 1u << st;
                 __syncwarp();
                 // a lane per (column block, run); 32 is a multiple of the runs, so a lane's run is its own
                 for (int i = lane; i < runs * (D / 64); i += 32) {
                     const int cb = i / runs;
                     tma_load_4d(base + S::KV + st * S::TILE + cb * kBlock + run * granule * 128,
-                                kv == 0 ? &maps.k : &maps.v, &b->kv_full[st], cb * 64, u.head, in_page, page);
+                                kv == 0 ? &maps.k : &maps.v, full, cb * 64, u.head, in_page, page);
                 }
                 __syncwarp();
                 ++ring;
@@ -322,153 +376,83 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
     if (!ok) {   // wait for this warp's own copies before the CTA may leave
         const unsigned n = min(ring, (unsigned)S::STAGES);
         for (unsigned i = ring - n; i < ring; ++i) mbar_wait_bounded(&b->kv_full[i % S::STAGES], (i / S::STAGES) & 1, kWaitNs);
+        for (int i = 0; i < S::STAGES; ++i)
+            if ((raw_any >> i) & 1) mbar_wait_bounded(&b->v_raw[i], ((raws >> i) & 1) ^ 1, kWaitNs);
         if (units) mbar_wait_bounded(&b->q_full, (units - 1) & 1, kWaitNs);
     }
 }
 
-// --------------------------------------------------------------- MMA issuer
+// --------------------------------------------------------------- MMA issuers
+// One thread per stream issues its products, in the order QK(h + 1), PV(h): the scores of a
+// step are computed while the softmax of the step before runs.  A warp for both streams,
+// with its waits and elections, took 2560 clocks a step, twice the tensor core's time.
 template <int D>
-__device__ __forceinline__ void mma_role(const Args& a, uint8_t* smem, Bars* b) {
+__device__ __forceinline__ void mma_role(const Args& a, uint8_t* smem, Bars* b, int s) {
     using S = Smem<D>;
-    const int lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem), tm = b->tmem;
-    const uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, D, false, true);
-    unsigned ring = 0, units = 0, p_count0 = 0, p_count1 = 0;
+    const uint32_t id_s = idesc_bf16(128, kStep, false, false), id_o = idesc_bf16(128, D, false, true);
+    unsigned tiles = 0, units = 0, steps = 0, cleaned = 0;   // before this piece; parities of v_clean
     bool ok = true;
-
-    auto k_stage = [&](int j) { return (ring + 2 * j) % S::STAGES; };
-    auto v_stage = [&](int j) { return (ring + 2 * j + 1) % S::STAGES; };
-    auto full = [&](unsigned at) { return wait(b, &b->kv_full[at % S::STAGES], (at / S::STAGES) & 1); };
-    // S of stream s = row tile `sub` times the keys in `stage`
-    auto scores = [&](int s, int sub, unsigned stage) {
-        const uint64_t dq = smem_desc_sw128(base + S::Q + sub * S::TILE, 16, 1024);
-        const uint64_t dk = smem_desc_sw128(base + S::KV + stage * S::TILE, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kBlock + (kk & 3) * 32;
-            mma_bf16_ss(tm + s * 128, desc_advance(dq, off), desc_advance(dk, off), id_s, kk > 0);
-        }
-        mma_commit(&b->s_full[s]);
-    };
-    auto values = [&](int s, unsigned stage, bool first) {
-        const uint64_t dv = smem_desc_sw128(base + S::KV + stage * S::TILE, kBlock, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_bf16_ts(tm + 256 + s * 128, tm + s * 128 + kk * 8, desc_advance(dv, kk * 2048), id_o,
-                        !first || kk > 0);
-    };
-
-    auto p_ready = [&](int s) {
-        const unsigned ph = s ? p_count1++ : p_count0++;
-        return wait(b, &b->p_ready[s], ph & 1);
-    };
-
     Pieces pieces;
-    for (Piece u = pieces.get(b); u.n > 0; u = pieces.get(b)) {
-        const int n = u.n;
-        // the V rows of tile j that hold no key of this unit become zero
-        auto clear_outside = [&](int j) {
-            const int key0 = u.key0 + j * kKeys;
-            const int from = max(0, u.lo - key0), to = min(kKeys, u.hi - key0);
-            if (from == 0 && to == kKeys) return;
-            const uint32_t tile = base + S::KV + v_stage(j) * S::TILE;
-            for (int i = lane; i < kKeys * (D / 64); i += 32) {
-                const int r = i % kKeys;
-                if (r >= from && r < to) continue;
-                const uint32_t at = tile + (i / kKeys) * kBlock + r * 128;
+    for (Piece u = pieces.get_one(b); u.n > 0; u = pieces.get_one(b)) {
+        // steps: single: step h is tile h, half s; else tile h / 2, half h % 2
+        const bool single = u.single;
+        const int H = single ? u.n : 2 * u.n;
+        const uint64_t dq = smem_desc_sw128(base + S::Q + (single ? 0 : s) * S::TILE, 16, 1024);
+        // S of step h into its buffer, over the P of step h - 2, whose product has to be
+        // complete: products into different accumulators are not ordered by their issue
+        auto scores = [&](int h) {
+            const unsigned G = steps + h, buf = G & 1, at = 2 * (tiles + (single ? h : h >> 1)), st = at % S::STAGES;
+            const int half = single ? s : h & 1;
+            if (single || half == 0) ok = wait_one(b, &b->kv_full[st], (at / S::STAGES) & 1);
+            if (ok && G >= 2) ok = wait_one(b, &b->o_step[2 * s + buf], ((G - 2) >> 1) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t dk = smem_desc_sw128(base + S::KV + st * S::TILE + half * (kStep * 128), 16, 1024);
+            const uint32_t d = tm + s * 128 + buf * 64;
 #pragma unroll
-                for (int c = 0; c < 128; c += 16)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + c), "r"(0) : "memory");
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * kBlock + (kk & 3) * 32;
+                mma_bf16_ss(d, desc_advance(dq, off), desc_advance(dk, off), id_s, kk > 0);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
+            mma_commit(&b->s_full[2 * s + buf]);
+            if (single || half == 1) mma_commit(&b->kv_free[st]);
+            if (h == H - 1) mma_commit(&b->q_free);
         };
-        ok = wait(b, &b->q_full, units & 1);
+        ok = wait_one(b, &b->q_full, units & 1);
         ++units;
-        if (!ok) break;
-        if (u.single) {
-            // stream s: tiles s, s + 2, ...
-            for (int j = 0; j < min(n, 2); ++j) {
-                ok = ok && full(ring + 2 * j);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    scores(j, 0, k_stage(j));
-                    mma_commit(&b->kv_free[k_stage(j)]);
-                    if (j + 1 == n) mma_commit(&b->q_free);
+        if (ok) scores(0);
+        for (int h = 0; ok && h < H; ++h) {
+            if (h + 1 < H) scores(h + 1);
+            if (!ok) break;
+            const unsigned G = steps + h, buf = G & 1, at = 2 * (tiles + (single ? h : h >> 1)) + 1, st = at % S::STAGES;
+            const int half = single ? s : h & 1;
+            if (single || half == 0) {
+                if (u.ragged(single ? h : h >> 1)) {   // the walker's word that it is clean
+                    ok = wait_one(b, &b->v_clean[st], (cleaned >> st) & 1);
+                    cleaned ^= 1u << st;
+                } else {
+                    ok = wait_one(b, &b->kv_full[st], (at / S::STAGES) & 1);
                 }
-                __syncwarp();
             }
-            for (int j = 0; ok && j < n; ++j) {
-                const int s = j & 1;
-                ok = full(ring + 2 * j + 1);
-                if (!ok) break;
-                clear_outside(j);
-                ok = p_ready(s);
-                if (ok && j + 2 < n) ok = full(ring + 2 * (j + 2));
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    values(s, v_stage(j), j < 2);
-                    mma_commit(&b->kv_free[v_stage(j)]);
-                    if (j + 2 < n) {
-                        scores(s, 0, k_stage(j + 2));
-                        mma_commit(&b->kv_free[k_stage(j + 2)]);
-                        if (j + 3 == n) mma_commit(&b->q_free);
-                    } else {
-                        mma_commit(&b->o_done[s]);
-                    }
-                }
-                __syncwarp();
-            }
-        } else {
-            ok = full(ring);
+            if (ok) ok = wait_one(b, &b->p_ready[2 * s + buf], (G >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-                scores(0, 0, k_stage(0));
-                scores(1, 1, k_stage(0));
-                mma_commit(&b->kv_free[k_stage(0)]);
-                if (n == 1) mma_commit(&b->q_free);
-            }
-            __syncwarp();
-            for (int j = 0; ok && j < n; ++j) {
-                const bool next = j + 1 < n;
-                ok = full(ring + 2 * j + 1);
-                if (ok && next) ok = full(ring + 2 * (j + 1));
-                if (!ok) break;
-                clear_outside(j);
+            const uint64_t dv = smem_desc_sw128(base + S::KV + st * S::TILE + half * (kStep * 128), kBlock, 1024);
+            const uint32_t d = tm + 256 + s * 128, p = tm + s * 128 + buf * 64;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    ok = ok && p_ready(s);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        values(s, v_stage(j), j == 0);
-                        if (s == 1) mma_commit(&b->kv_free[v_stage(j)]);
-                        if (next) {
-                            scores(s, s, k_stage(j + 1));
-                            if (s == 1) {
-                                mma_commit(&b->kv_free[k_stage(j + 1)]);
-                                if (j + 2 == n) mma_commit(&b->q_free);
-                            }
-                        } else {
-                            mma_commit(&b->o_done[s]);
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
+            for (int kk = 0; kk < kStep / 16; ++kk)
+                mma_bf16_ts(d, p + kk * 8, desc_advance(dv, kk * 2048), id_o, h > 0 || kk > 0);
+            mma_commit(&b->o_step[2 * s + buf]);
+            if (single || half == 1) mma_commit(&b->kv_free[st]);
         }
         if (!ok) break;
-        ring += 2 * n;
+        tiles += u.n;
+        steps += H;
     }
     // everything issued is complete before the TMEM goes back
-    if (elect_one()) {
-        mma_commit(&b->drain);
-        mbar_wait_bounded(&b->drain, 0, kWaitNs);
-    }
-    __syncwarp();
+    mma_commit(&b->drain[s]);
+    mbar_wait_bounded(&b->drain[s], 0, kWaitNs);
 }
 
 // ------------------------------------------------------------ softmax groups
@@ -478,10 +462,10 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int row = quarter * 32 + lane;
     const uint32_t tm = b->tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t tm_s = tm + s * 128, tm_o = tm + 256 + s * 128;
+    const uint32_t tm_o = tm + 256 + s * 128;
     float* exch = reinterpret_cast<float*>(smem + S::EXCH);
     const float sl = a.scale * 1.4426950408889634f;
-    unsigned s_count = 0, o_count = 0, x_count = 0;
+    unsigned steps = 0, x_count = 0;   // steps of this stream, over all pieces
     bool ok = true;
     Pieces pieces;
     for (Piece u = pieces.get(b); u.n > 0; u = pieces.get(b)) {
@@ -496,37 +480,44 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         const int all_lo = a.window > 0 ? max(0, first_pos + toks - a.window) : 0;
         const bool active = quarter * 32 < rows;   // this warp has rows
         float m = -INFINITY, l = 0.0f;
-        bool any_tile = false;
-        for (int j = u.single ? s : 0; j < u.n; j += u.single ? 2 : 1) {
-            ok = wait(b, &b->s_full[s], s_count++ & 1);
+        const int H = u.single ? u.n : 2 * u.n;
+        for (int h = 0; h < H; ++h, ++steps) {
+            const unsigned buf = steps & 1;
+            const uint32_t tm_s = tm + s * 128 + buf * 64;
+            ok = wait(b, &b->s_full[2 * s + buf], (steps >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             if (active) {
-                const int key0 = u.key0 + j * kKeys;
-                float x[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + c * 32, x + c * 32);
+                const int key0 = u.key0 + (u.single ? 2 * h + s : h) * kStep;
+                float x[kStep];
+                tmem_ld32(tm_s, x);
+                tmem_ld32(tm_s + 32, x + 32);
                 tmem_wait_ld();
-                const bool masked = key0 < all_lo || key0 + kKeys - 1 > all_hi;
+                const bool masked = key0 < all_lo || key0 + kStep - 1 > all_hi;
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
+                    for (int i = 0; i < kStep; ++i)
                         x[i] = key0 + i >= low_key && key0 + i <= top_key ? x[i] : -INFINITY;
                 }
                 float t0 = max3(m, x[0], x[1]), t1 = max3(x[2], x[3], x[4]), t2 = max3(x[5], x[6], x[7]);
 #pragma unroll
-                for (int i = 8; i < 128; i += 6) {
+                for (int i = 8; i < 62; i += 6) {
                     t0 = max3(t0, x[i], x[i + 1]);
                     t1 = max3(t1, x[i + 2], x[i + 3]);
                     t2 = max3(t2, x[i + 4], x[i + 5]);
                 }
+                t0 = max3(t0, x[62], x[63]);
                 const float top = max3(t0, t1, t2);
-                // (also when a NaN came in; not when all is still masked)
-                if (__any_sync(0xffffffffu, !((top - m) * sl <= kLazy) && top != -INFINITY)) {
-                    const float f = m == -INFINITY ? 0.0f : ex2((m - top) * sl);
+                // also when a NaN came in; not when all is still masked, nor for rows that are
+                // no rows.  Each row decides for itself: what shares its warp changes no bit of it.
+                const bool grown = row < rows && !((top - m) * sl <= kLazy) && top != -INFINITY;
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float f = !grown ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - top) * sl);
                     l *= f;
-                    m = top;
-                    if (any_tile) {   // the last product into O is complete: this tile's scores came behind it
+                    m = grown ? top : m;
+                    if (h > 0) {   // the last product into O, if it is not complete yet
+                        ok = wait(b, &b->o_step[2 * s + (buf ^ 1)], ((steps - 1) >> 1) & 1);
+                        tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
@@ -542,16 +533,15 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                 l += masked ? probabilities<0>(x, sl, off, tm_s) : probabilities<kPoly>(x, sl, off, tm_s);
                 tmem_wait_st();
             }
-            any_tile = true;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&b->p_ready[s]);
+            if (lane == 0) mbar_arrive(&b->p_ready[2 * s + buf]);
         }
-        if (ok && any_tile) ok = wait(b, &b->o_done[s], o_count++ & 1);
+        if (ok) ok = wait(b, &b->o_step[2 * s + ((steps - 1) & 1)], ((steps - 1) >> 1) & 1);
         if (!ok) break;
         if (u.single) {   // both streams' outputs are complete, their maxima and sums exchanged
-            exch[s * 256 + row] = any_tile && active ? m : -INFINITY;
-            exch[s * 256 + 128 + row] = any_tile && active ? l : 0.0f;
+            exch[s * 256 + row] = m;
+            exch[s * 256 + 128 + row] = l;
             __syncwarp();
             if (lane == 0) mbar_arrive(&b->x_full);
             ok = wait(b, &b->x_full, x_count & 1);
@@ -571,14 +561,12 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         if (active) {
             // weights of the two streams' sums (the other stream has other rows: 0)
             float f0 = 1.0f, f1 = 0.0f, sum = l, top = m;
-            bool both = false;
             if (u.single) {
                 const float m0 = exch[row], l0 = exch[128 + row], m1 = exch[256 + row], l1 = exch[256 + 128 + row];
                 top = fmaxf(m0, m1);
                 f0 = m0 == -INFINITY ? 0.0f : ex2((m0 - top) * sl);
                 f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - top) * sl);
                 sum = l0 * f0 + l1 * f1;
-                both = u.n > 1;          // the second stream had a tile
             }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             f0 *= inv;
@@ -592,7 +580,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] *= f0;
-                if (both) {
+                if (u.single) {
                     float z[32];
                     tmem_ld32(from + 128 + c * 32, z);
                     tmem_wait_ld();
@@ -704,20 +692,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0) {
         mbar_init(&b->q_full, 1);
-        mbar_init(&b->q_free, 1);
-        mbar_init(&b->drain, 1);
+        mbar_init(&b->q_free, 2);
         mbar_init(&b->x_full, 8);
         mbar_init(&b->x_free, 8);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&b->s_full[s], 1);
-            mbar_init(&b->p_ready[s], 4);
-            mbar_init(&b->o_done[s], 1);
             mbar_init(&b->piece_full[s], 1);
-            mbar_init(&b->piece_free[s], 10);   // the softmax, MMA and loader warps
+            mbar_init(&b->piece_free[s], 11);   // the softmax and MMA warps, the loader
+            mbar_init(&b->drain[s], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&b->s_full[i], 1);
+            mbar_init(&b->p_ready[i], 4);
+            mbar_init(&b->o_step[i], 1);
         }
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(&b->kv_full[i], 1);
-            mbar_init(&b->kv_free[i], 1);
+            mbar_init(&b->kv_free[i], 2);       // both streams
+            mbar_init(&b->v_raw[i], 1);
+            mbar_init(&b->v_clean[i], 1);
         }
         b->abort = b->bad_page = 0;
         mbar_fence_init();
@@ -726,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&b->tmem, 512);
         tmem_relinquish();
     }
-    if (warp == 9 && elect_one()) {
+    if (warp == 10 && elect_one()) {
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -735,13 +727,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         softmax_role<D>(a, smem, b, warp >> 2);
+    } else if (warp < 10) {
+        if (elect_one()) mma_role<D>(a, smem, b, warp - 8);
+        __syncwarp();
+    } else if (warp == 10) {
+        load_role<D>(a, maps, smem, b, granule);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8) mma_role<D>(a, smem, b);
-        else if (warp == 9) load_role<D>(a, maps, smem, b, granule);
-        else if (warp == 10) walk_role(a, ln, b);
+        walk_role<D>(a, ln, smem, b);
     }
     tc_fence_before();
     __syncthreads();
