@@ -50,7 +50,7 @@ constexpr int kMaxParts = 148;     // one CTA per SM of a B200
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a row's maximum that P absorbs
-constexpr int kPoly = 4;           // of 16 pairs of exponentials, those on the FMA pipe (measured: 0 .. 8)
+constexpr int kPoly = 5;           // of 16 pairs of exponentials, those on the FMA pipe (measured: 0 .. 8)
 constexpr int kMerge = 4;          // parts of a split unit read at once
 constexpr int kBlock = kKeys * 128;   // bytes of one 64-column block of a 128-row tile
 
@@ -118,6 +118,7 @@ __device__ __forceinline__ bool wait_one(Bars* b, uint64_t* bar, uint32_t parity
 
 // The same by a whole warp, every lane with the same answer.
 __device__ __forceinline__ bool wait(Bars* b, uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, wait_one(b, bar, parity));
 }
 
@@ -165,40 +166,39 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return y;
 }
 
-// 2^y of both halves on the FMA pipe, for y in [-127, 128) (below: about 2^-127).  y = n + f
+// 2^y of both halves on the FMA pipe, for y < 128; exactly 0 at and below -127.  y = n + f
 // with n the nearest integer (found by adding 1.5 * 2^23, whose low bits then hold it), 2^f a
-// polynomial of degree 5 with the least relative error on [-1/2, 1/2] (a Remez fit of its
-// own: 7.5e-8, as fp32 arithmetic 2.4e-7), n added to its exponent.
+// polynomial of degree 5 with value 1 at 0 and else the least relative error on [-1/2, 1/2]
+// (a Remez fit of its own: 4.9e-7 in fp32 arithmetic, twice the special function unit's),
+// n added to its exponent: -127 leaves none of 1.0's.
 __device__ __forceinline__ float2 ex2_poly(Pair y) {
     const float2 in = unpair(y);
     y = pair(fmaxf(in.x, -127.0f), fmaxf(in.y, -127.0f));
     const Pair t = add2(y, pair(12582912.0f, 12582912.0f));
     const Pair n = add2(t, pair(-12582912.0f, -12582912.0f));
     const Pair f = fma2(n, pair(-1.0f, -1.0f), y);
-    Pair p = pair(0.0013276472454890609f, 0.0013276472454890609f);
-    p = fma2(p, f, pair(0.009675540961325169f, 0.009675540961325169f));
-    p = fma2(p, f, pair(0.05550713092088699f, 0.05550713092088699f));
-    p = fma2(p, f, pair(0.24022120237350464f, 0.24022120237350464f));
-    p = fma2(p, f, pair(0.6931469440460205f, 0.6931469440460205f));
-    p = fma2(p, f, pair(1.0000001192092896f, 1.0000001192092896f));
+    Pair p = pair(0.0011125507298856974f, 0.0011125507298856974f);
+    p = fma2(p, f, pair(0.009666282683610916f, 0.009666282683610916f));
+    p = fma2(p, f, pair(0.05557400360703468f, 0.05557400360703468f));
+    p = fma2(p, f, pair(0.24022351205348969f, 0.24022351205348969f));
+    p = fma2(p, f, pair(0.693142831325531f, 0.693142831325531f));
+    p = fma2(p, f, pair(1.0f, 1.0f));
     const float2 e = unpair(p), k = unpair(t);
     return make_float2(__uint_as_float(__float_as_uint(e.x) + (__float_as_uint(k.x) << 23)),
                        __uint_as_float(__float_as_uint(e.y) + (__float_as_uint(k.y) << 23)));
 }
 
-// One row's P from its 64 scores of a step: 2^(s scale - m scale) as bf16 into TMEM, their sum
-// returned.  Of 16 pairs, POLY go through the polynomial: the special function unit alone
-// (16 results a clock and SM) would need 2048 clocks per 128 keys of both streams.  (POLY = 0 on tiles with masked keys, whose P must be 0 exactly.)
+// P of a step's scores of one row, 2^(s scale - m scale), as bf16 into 32 TMEM columns; their
+// sum is added to sum.  Of 16 pairs, POLY go through the polynomial: the special function
+// unit alone (16 results a clock and SM) would need 2048 clocks per 128 keys of both streams.
 template <int POLY>
-__device__ __forceinline__ float probabilities(const float* x, float scale, float off, uint32_t to) {
-    const Pair sc = pair(scale, scale), of = pair(off, off);
-    Pair sum[2] = {0ull, 0ull};
+__device__ __forceinline__ void probabilities(const float* x, Pair scale, Pair off, uint32_t to, Pair* sum) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < kStep / 32; ++c) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const Pair y = fma2(pair(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), sc, of);
+            const Pair y = fma2(pair(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), scale, off);
             float2 e;
             if ((i * POLY) % 16 < POLY && POLY > 0) {
                 e = ex2_poly(y);
@@ -212,8 +212,18 @@ __device__ __forceinline__ float probabilities(const float* x, float scale, floa
         }
         tmem_st16(to + c * 16, p);
     }
-    const float2 a = unpair(add2(sum[0], sum[1]));
-    return a.x + a.y;
+}
+
+// After a wait for TMEM loads: ties 32 loaded values to this point, so that the compiler
+// computes nothing with them before it.
+__device__ __forceinline__ void loaded32(float* x) {
+    asm volatile(""
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]),
+                   "+f"(x[6]), "+f"(x[7]), "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]),
+                   "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]), "+f"(x[16]), "+f"(x[17]),
+                   "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]),
+                   "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]),
+                   "+f"(x[30]), "+f"(x[31]));
 }
 
 // ------------------------------------------------------------------- walker
@@ -479,7 +489,9 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         const int all_hi = first_pos;
         const int all_lo = a.window > 0 ? max(0, first_pos + toks - a.window) : 0;
         const bool active = quarter * 32 < rows;   // this warp has rows
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY;
+        const Pair scale = pair(sl, sl);
+        Pair sum[2] = {0ull, 0ull};
         const int H = u.single ? u.n : 2 * u.n;
         for (int h = 0; h < H; ++h, ++steps) {
             const unsigned buf = steps & 1;
@@ -493,11 +505,17 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                 tmem_ld32(tm_s, x);
                 tmem_ld32(tm_s + 32, x + 32);
                 tmem_wait_ld();
+                loaded32(x);
+                loaded32(x + 32);
                 const bool masked = key0 < all_lo || key0 + kStep - 1 > all_hi;
                 if (masked) {
+                    // the keys of the step that this row sees, a bit each
+                    const int end = top_key - key0 + 1, begin = low_key - key0;
+                    const unsigned long long seen =
+                        (end >= kStep ? ~0ull : end <= 0 ? 0ull : (1ull << end) - 1) &
+                        (begin <= 0 ? ~0ull : begin >= kStep ? 0ull : ~0ull << begin);
 #pragma unroll
-                    for (int i = 0; i < kStep; ++i)
-                        x[i] = key0 + i >= low_key && key0 + i <= top_key ? x[i] : -INFINITY;
+                    for (int i = 0; i < kStep; ++i) x[i] = (seen >> i) & 1 ? x[i] : -INFINITY;
                 }
                 float t0 = max3(m, x[0], x[1]), t1 = max3(x[2], x[3], x[4]), t2 = max3(x[5], x[6], x[7]);
 #pragma unroll
@@ -513,12 +531,13 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                 const bool grown = row < rows && !((top - m) * sl <= kLazy) && top != -INFINITY;
                 if (__any_sync(0xffffffffu, grown)) {
                     const float f = !grown ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - top) * sl);
-                    l *= f;
+                    sum[0] = fma2(sum[0], pair(f, f), 0ull);
+                    sum[1] = fma2(sum[1], pair(f, f), 0ull);
                     m = grown ? top : m;
                     if (h > 0) {   // the last product into O, if it is not complete yet
                         ok = wait(b, &b->o_step[2 * s + (buf ^ 1)], ((steps - 1) >> 1) & 1);
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1   // small, beside the hot path
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
                             tmem_ld16(tm_o + c * 16, o);
@@ -530,13 +549,15 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                     }
                 }
                 const float off = m == -INFINITY ? 0.0f : -m * sl;
-                l += masked ? probabilities<0>(x, sl, off, tm_s) : probabilities<kPoly>(x, sl, off, tm_s);
+                probabilities<kPoly>(x, scale, pair(off, off), tm_s, sum);
                 tmem_wait_st();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b->p_ready[2 * s + buf]);
         }
+        const float2 sums = unpair(add2(sum[0], sum[1]));
+        const float l = sums.x + sums.y;
         if (ok) ok = wait(b, &b->o_step[2 * s + ((steps - 1) & 1)], ((steps - 1) >> 1) & 1);
         if (!ok) break;
         if (u.single) {   // both streams' outputs are complete, their maxima and sums exchanged
