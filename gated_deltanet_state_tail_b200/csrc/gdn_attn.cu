@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
     const long long per = ln.per_part;
     long long pos = (long long)blockIdx.x * per;
     const long long end = min(pos + per, ln.total);
-    Unit u = find_unit(a, pos);
+    const StoredSeqs seqs{a};
+    Unit u = find_unit(a, seqs, pos);
     const float scale = a.scale * kLog2e;
     bool begins = true;
     for (;;) {
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
         pos = u.begin + kt1;
         begins = false;
         if (pos >= end) break;
-        next_unit(a, u);
+        next_unit(a, seqs, u);
     }
 }
 
@@ -374,6 +375,7 @@ cudaError_t launch_paged_attention(const attn::Args& args, cudaStream_t stream) 
     // many token blocks to go through (32: under a microsecond); a launch less.
     const long long step = (long long)a.block_tokens * a.shape.subs;
     a.line_inline = a.batch <= a.shape.threads && (a.rows + step - 1) / step <= 32;
+    if (a.line_inline && a.batch <= 32 && a.dtype == GDN_BF16) a.line_inline = 2;   // no block barrier before the first loads
     if (!a.line_inline) {
         attn::line_kernel<<<1, 1024, 0, stream>>>(a);
         const cudaError_t e = cudaGetLastError();

@@ -77,7 +77,7 @@ struct Args {
     float* lse;                             // [rows, num_heads] or null
     WorkspaceHeader* ws;
     unsigned int epoch;
-    int line_inline;                        // every CTA lays out the line itself
+    int line_inline;                        // every CTA lays out the line itself; 2: each of its warps that needs it
     Line* line;
     Seq* seqs;                              // [batch]
     unsigned long long* arrivals;           // [max_parts * kArrivals]: parts of split units that are in
@@ -123,23 +123,54 @@ struct Unit {
     long long begin;     // tile of the line where it begins
 };
 
-// The unit that holds tile `pos` of the line (0 <= pos < total), by a whole warp.
-__device__ __forceinline__ Unit find_unit(const Args& a, long long pos) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = a.batch;                        // the last sequence with before <= pos is in [lo, hi)
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int i = lo + lane * step;
-        const bool below = i < hi && a.seqs[i].before <= pos;
-        const int n = __popc(__ballot_sync(0xffffffffu, below));   // lane 0 is always below
-        lo = lo + (n - 1) * step;
-        hi = min(hi, lo + step);
+// The sequences of the line as find_unit and next_unit see them, for a whole warp: in the
+// workspace, or (at most 32) one per lane.
+struct StoredSeqs {
+    const Args& a;
+    __device__ __forceinline__ Seq get(int b) const { return a.seqs[b]; }
+    // the last sequence with before <= pos
+    __device__ __forceinline__ int find(long long pos) const {
+        const int lane = threadIdx.x & 31;
+        int lo = 0, hi = a.batch;                    // it is in [lo, hi)
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int i = lo + lane * step;
+            const bool below = i < hi && a.seqs[i].before <= pos;
+            const int n = __popc(__ballot_sync(0xffffffffu, below));   // lane 0 is always below
+            lo = lo + (n - 1) * step;
+            hi = min(hi, lo + step);
+        }
+        return lo;
     }
+};
+struct LaneSeqs {
+    const Args& a;
+    Seq mine;
+    __device__ __forceinline__ Seq get(int b) const {
+        Seq s;
+        s.row0 = __shfl_sync(0xffffffffu, mine.row0, b);
+        s.qlen = __shfl_sync(0xffffffffu, mine.qlen, b);
+        s.ctx = __shfl_sync(0xffffffffu, mine.ctx, b);
+        s.pad = 0;
+        s.head_tiles = __shfl_sync(0xffffffffu, mine.head_tiles, b);
+        s.before = __shfl_sync(0xffffffffu, mine.before, b);
+        return s;
+    }
+    __device__ __forceinline__ int find(long long pos) const {
+        return 31 - __clz(__ballot_sync(0xffffffffu, (int)(threadIdx.x & 31) < a.batch && mine.before <= pos));
+    }
+};
+
+// The unit that holds tile `pos` of the line (0 <= pos < total), by a whole warp.
+template <typename Seqs>
+__device__ __forceinline__ Unit find_unit(const Args& a, const Seqs& seqs, long long pos) {
+    const int lane = threadIdx.x & 31;
     Unit u;
-    u.b = lo;
-    u.s = a.seqs[lo];
+    u.b = seqs.find(pos);
+    u.s = seqs.get(u.b);
     const long long in = pos - u.s.before;
-    u.head = (int)(in / u.s.head_tiles);
+    u.head = ((in | u.s.head_tiles) >> 32) ? (int)(in / u.s.head_tiles)
+                                           : (int)((uint32_t)in / (uint32_t)u.s.head_tiles);
     const long long rem = in - u.head * u.s.head_tiles;
     const int blocks = token_blocks(a, u.s.qlen);
     long long done = 0;
@@ -156,8 +187,7 @@ __device__ __forceinline__ Unit find_unit(const Args& a, long long pos) {
         if (hit || t0 + 32 >= blocks) {
             const int l = hit ? __ffs(hit) - 1 : 31;
             u.t = t0 + l;
-            u.begin = u.s.before + u.head * u.s.head_tiles + done +
-                      __shfl_sync(0xffffffffu, incl - n, l);
+            u.begin = u.s.before + u.head * u.s.head_tiles + done + __shfl_sync(0xffffffffu, incl - n, l);
             break;
         }
         done += __shfl_sync(0xffffffffu, incl, 31);
@@ -167,7 +197,8 @@ __device__ __forceinline__ Unit find_unit(const Args& a, long long pos) {
 }
 
 // The unit after u on the line (the caller knows that there is one).
-__device__ __forceinline__ void next_unit(const Args& a, Unit& u) {
+template <typename Seqs>
+__device__ __forceinline__ void next_unit(const Args& a, const Seqs& seqs, Unit& u) {
     u.begin += u.r.tiles;
     if (++u.t >= token_blocks(a, u.s.qlen)) {
         u.t = 0;
@@ -176,7 +207,7 @@ __device__ __forceinline__ void next_unit(const Args& a, Unit& u) {
             do {
                 ++u.b;
                 if (u.b >= a.batch) return;
-                u.s = a.seqs[u.b];
+                u.s = seqs.get(u.b);
             } while (u.s.qlen == 0);
         }
     }
@@ -213,6 +244,27 @@ __device__ __forceinline__ Line make_line(const Args& a, long long total) {
     ln.per_part = max((total + a.shape.max_parts - 1) / a.shape.max_parts, (long long)a.shape.min_tiles);
     ln.parts = (int)((total + ln.per_part - 1) / ln.per_part);
     return ln;
+}
+
+// The line of at most 32 sequences, by a whole warp: sequence b in lane b.
+__device__ __forceinline__ Line lane_line(const Args& a, LaneSeqs& seqs) {
+    const int lane = threadIdx.x & 31;
+    seqs.mine = Seq{0, 0, 0, 0, 0, 0};
+    long long n = 0;
+    if (lane < a.batch) {
+        bool good;
+        seqs.mine = load_seq<false>(a, lane, good);
+        if (!good) tag_merge_inline(&a.ws->status, a.epoch, kStatusMismatch, false);
+        n = seqs.mine.head_tiles * a.num_kv_heads;
+    }
+    long long incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += x;
+    }
+    seqs.mine.before = incl - n;
+    return make_line(a, __shfl_sync(0xffffffffu, incl, 31));
 }
 
 // The line as this CTA sees it, by every thread of a block of THREADS; ends with a block

@@ -51,7 +51,7 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a row's maximum that P absorbs
 constexpr int kPoly = 5;           // of 16 pairs of exponentials, those on the FMA pipe (measured: 0 .. 8)
-constexpr int kMerge = 4;          // parts of a split unit read at once
+constexpr int kMerge = 6;          // parts of a split unit read at once
 constexpr int kBlock = kKeys * 128;   // bytes of one 64-column block of a 128-row tile
 
 template <int D>
@@ -230,15 +230,16 @@ __device__ __forceinline__ void loaded32(float* x) {
 // Walks this CTA's stretch of the line and hands out its pieces, one ahead of the one in
 // work, whose tiles with rows outside the unit's keys it tends: their V rows there become
 // zero before the MMA warps use the tile.
-template <int D>
-__device__ __forceinline__ void walk_role(const Args& a, const Line& ln, uint8_t* smem, Bars* b) {
+template <int D, typename Seqs>
+__device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const Seqs& seqs, uint8_t* smem, Bars* b) {
     using S = Smem<D>;
     const int lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
     const long long per = ln.per_part;
     long long pos = (long long)blockIdx.x * per;
     const long long end = min(pos + per, ln.total);
-    Unit u = find_unit(a, pos);
+    Unit u{};
+    if (pos < end) u = find_unit(a, seqs, pos);
     unsigned tiles = 0, tended = 0;   // before the piece being tended; parities of v_raw
     Piece last;
     last.n = 0;
@@ -289,7 +290,7 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, uint8_t
         }
         last = p;
         if (p.n == 0) return;
-        if (pos < end) next_unit(a, u);
+        if (pos < end) next_unit(a, seqs, u);
     }
 }
 
@@ -705,8 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars* b = reinterpret_cast<Bars*>(smem + S::BARS);
     const int warp = threadIdx.x >> 5;
-    const Line ln = get_line<kThreads>(a, reinterpret_cast<long long*>(smem + S::SCAN));
-    if ((int)blockIdx.x >= ln.parts) return;
+    Line ln;
+    if (a.line_inline != 2) {
+        ln = get_line<kThreads>(a, reinterpret_cast<long long*>(smem + S::SCAN));
+        if ((int)blockIdx.x >= ln.parts) return;
+    } else if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.ws->epoch = a.epoch;
+    }
     if (smem_u32(smem) & 1023u) {   // the swizzled tiles need it; the runtime places the block's memory so
         if (threadIdx.x == 0) tag_merge_inline(&a.ws->status, a.epoch, kStatusBounds, false);
         return;
@@ -755,7 +761,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 10) {
         load_role<D>(a, maps, smem, b, granule);
     } else {
-        walk_role<D>(a, ln, smem, b);
+        if (a.line_inline == 2) {
+            LaneSeqs seqs{a};
+            ln = lane_line(a, seqs);
+            walk_role<D>(a, ln, seqs, smem, b);
+        } else {
+            walk_role<D>(a, ln, StoredSeqs{a}, smem, b);
+        }
     }
     tc_fence_before();
     __syncthreads();
