@@ -16,6 +16,7 @@ full-attention layers of the hybrid stack have ``qk_norm_rope`` and
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -404,17 +405,33 @@ def gdn_workspace_status(workspace, stream=None) -> int:
 # The operators below are called once per layer and token, so their argument checks are
 # written to cost little: no torch import, stream object or library lookup per call.
 
-def _row_stride(t, heads, dim, name):
+_torch_module = None
+_codes = {}
+
+
+def _torch():
+    """torch, imported at the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _codes.update({torch.float32: GDN_F32, torch.bfloat16: GDN_BF16})
+        _torch_module = torch
+    return _torch_module
+
+
+def _code(dtype):
+    code = _codes.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _row_stride(shape, stride, name):
     """Row stride (elements; 0 = packed) of a [rows, heads, dim] view with contiguous heads inside a row."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [rows, heads, head_dim]")
-    rows, h, d = t.shape
-    if h != heads or d != dim:
-        raise ValueError(f"{name} must be [rows, {heads}, {dim}]")
-    s0, s1, s2 = t.stride()
-    if rows and (s2 != 1 or (heads > 1 and s1 != dim)):
+    rows, heads, dim = shape
+    if rows and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
         raise ValueError(f"{name} must have contiguous heads inside a row")
-    return s0 if rows > 1 else 0
+    return stride[0] if rows > 1 else 0
 
 
 def _dense(t, shape, dtype, name):
@@ -431,17 +448,6 @@ def _launch_device(*tensors):
     if here < 0 or here != _torch().cuda.current_device():
         raise ValueError("every tensor must be on the current CUDA device")
     return here
-
-
-_torch_module = None
-
-
-def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
 
 
 def _launch_stream(stream, device):
@@ -465,18 +471,35 @@ def _fn(name):
     return f
 
 
+# Descriptors by their fields: a program's calls repeat a few shapes.  The structures are never changed.
+@functools.lru_cache(maxsize=256)
+def _kv_desc(shape, stride, packed, code):
+    if len(shape) != 4 or stride[3] != 1:
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim] with contiguous "
+                         "elements inside a head")
+    return gdn_paged_kv(*shape, code, 0, *((0, 0, 0) if packed else stride[:3]))
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_desc(*fields):
+    return gdn_qk_desc(*fields)
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_desc(*fields):
+    return gdn_attn_desc(*fields)
+
+
 def _paged_kv(k_cache, v_cache):
     """Descriptor of [num_pages, page_size, num_kv_heads, head_dim] key and value pools (any strides with
     contiguous elements inside a head, the same for both)."""
-    shape, stride = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or shape != v_cache.shape or k_cache.dtype is not v_cache.dtype:
-        raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim], alike")
-    if stride != v_cache.stride() or stride[3] != 1:
-        raise ValueError("k_cache and v_cache must share their strides, with contiguous elements inside a head")
-    pages, page, heads, dim = shape
-    if k_cache.is_contiguous():
-        return gdn_paged_kv(pages, page, heads, dim, _dtype_code(k_cache.dtype), 0, 0, 0, 0)
-    return gdn_paged_kv(pages, page, heads, dim, _dtype_code(k_cache.dtype), 0, *stride[:3])
+    shape, stride, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if shape != v_cache.shape or dtype is not v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be alike")
+    if stride != v_cache.stride():
+        raise ValueError("k_cache and v_cache must share their strides")
+    _torch()
+    return _kv_desc(shape, stride, k_cache.is_contiguous(), _code(dtype))
 
 
 def gdn_qk_norm_rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, k_cache, v_cache, slots, q_out, k_out,
@@ -484,31 +507,33 @@ def gdn_qk_norm_rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, k_ca
     """Norm, rotation and cache append (see ``qk_norm_rope``); every output is given."""
     torch = _torch()
     device = _launch_device(q, k, v, positions, inv_freq, q_weight, k_weight, k_cache, v_cache, slots, q_out, k_out)
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    q_shape, k_shape, dtype = q.shape, k.shape, q.dtype
+    if len(q_shape) != 3 or len(k_shape) != 3 or q_shape[0] != k_shape[0] or q_shape[2] != k_shape[2]:
         raise ValueError("q must be [rows, num_heads, head_dim] and k [rows, num_kv_heads, head_dim]")
-    rows, heads, dim = q.shape
-    kv = k.shape[1]
-    dtype = q.dtype
+    rows, heads, dim = q_shape
     if k.dtype is not dtype or (v is not None and v.dtype is not dtype):
         raise ValueError("q, k and v must have one dtype")
-    rot = 0
+    half, pos_ptr, freq_ptr, qw_ptr, kw_ptr, ko_ptr = 0, None, None, None, None, None
     if inv_freq is not None:
         half = inv_freq.numel()
-        rot = 2 * half
         _dense(inv_freq, (half,), torch.float64, "inv_freq")
         _dense(positions, (rows,), torch.int64, "positions")
+        pos_ptr, freq_ptr = positions.data_ptr(), inv_freq.data_ptr()
     if q_weight is not None:
         _dense(q_weight, (dim,), torch.float32, "q_weight")
+        qw_ptr = q_weight.data_ptr()
     if k_weight is not None:
         _dense(k_weight, (dim,), torch.float32, "k_weight")
-    _dense(q_out, (rows, heads, dim), dtype, "q_out")
+        kw_ptr = k_weight.data_ptr()
+    _dense(q_out, q_shape, dtype, "q_out")
     if k_out is not None:
-        _dense(k_out, (rows, kv, dim), dtype, "k_out")
+        _dense(k_out, k_shape, dtype, "k_out")
+        ko_ptr = k_out.data_ptr()
     cache, v_stride, v_ptr, k_pages, v_pages, slot_ptr = None, 0, None, None, None, None
     if k_cache is not None:
-        if v is None or v_cache is None or slots is None or v.shape[0] != rows:
-            raise ValueError("a cache needs v, v_cache and slots, one row of each per row of k")
-        v_stride = _row_stride(v, kv, dim, "v")
+        if v is None or v_cache is None or slots is None or v.shape != k_shape:
+            raise ValueError("a cache needs v (shaped like k), v_cache and slots")
+        v_stride = _row_stride(k_shape, v.stride(), "v")
         _dense(slots, (rows,), torch.int64, "slots")
         if k_cache.dtype is not dtype:
             raise ValueError("the cache must have the dtype of q, k and v")
@@ -516,16 +541,22 @@ def gdn_qk_norm_rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, k_ca
         v_ptr, k_pages, v_pages, slot_ptr = v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
     elif slots is not None or v_cache is not None:
         raise ValueError("slots and v_cache need k_cache")
-    d = gdn_qk_desc(rows, heads, kv, dim, rot, GDN_ROTARY_INTERLEAVED if interleaved else GDN_ROTARY_HALVES,
-                    _dtype_code(dtype), _row_stride(q, heads, dim, "q"), _row_stride(k, kv, dim, "k"), v_stride)
-    _check(_fn("gdn_qk_norm_rope")(
-        ctypes.byref(d), q.data_ptr(), k.data_ptr(), v_ptr, _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
-        _ptr(k_weight), eps, cache, slot_ptr, k_pages, v_pages, q_out.data_ptr(), _ptr(k_out),
-        _launch_stream(stream, device)), "gdn_qk_norm_rope")
+    d = _qk_desc(rows, heads, k_shape[1], dim, 2 * half, GDN_ROTARY_INTERLEAVED if interleaved else GDN_ROTARY_HALVES,
+                 _code(dtype), _row_stride(q_shape, q.stride(), "q"), _row_stride(k_shape, k.stride(), "k"), v_stride)
+    status = _fn("gdn_qk_norm_rope")(
+        ctypes.byref(d), q.data_ptr(), k.data_ptr(), v_ptr, pos_ptr, freq_ptr, qw_ptr, kw_ptr, eps, cache, slot_ptr,
+        k_pages, v_pages, q_out.data_ptr(), ko_ptr, _launch_stream(stream, device))
+    if status:
+        _check(status, "gdn_qk_norm_rope")
 
 
 def gdn_paged_attention_workspace_bytes(dtype, head_dim, max_batch) -> int:
     return int(_fn("gdn_paged_attention_workspace_bytes")(_dtype_code(dtype), int(head_dim), int(max_batch)))
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(code, dim, batch):
+    return int(_fn("gdn_paged_attention_workspace_bytes")(code, dim, batch))
 
 
 def gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace, scale=None,
@@ -534,31 +565,34 @@ def gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len
     torch = _torch()
     device = _launch_device(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace)
     c = _paged_kv(k_cache, v_cache)
-    if q.dim() != 3 or q.dtype is not k_cache.dtype:
+    q_shape, t_shape = q.shape, page_table.shape
+    if len(q_shape) != 3 or q.dtype is not k_cache.dtype:
         raise ValueError("q must be [rows, num_heads, head_dim] of the cache's dtype")
-    rows, heads, dim = q.shape
+    rows, heads, dim = q_shape
     if dim != c.head_dim:
         raise ValueError("q and the cache must have one head_dim")
-    if page_table.dim() != 2:
+    if len(t_shape) != 2:
         raise ValueError("page_table must be [batch, max_pages]")
-    batch, width = page_table.shape
-    _dense(page_table, (batch, width), torch.int32, "page_table")
+    batch, width = t_shape
+    _dense(page_table, t_shape, torch.int32, "page_table")
     _dense(cu_seqlens, (batch + 1,), torch.int32, "cu_seqlens")
     _dense(context_len, (batch,), torch.int32, "context_len")
-    _dense(o_out, (rows, heads, dim), q.dtype, "o_out")
+    _dense(o_out, q_shape, q.dtype, "o_out")
+    lse_ptr = None
     if lse_out is not None:
         _dense(lse_out, (rows, heads), torch.float32, "lse_out")
-    if not workspace.is_contiguous():
-        raise ValueError("the workspace must be contiguous")
-    need = _fn("gdn_paged_attention_workspace_bytes")(c.dtype, dim, batch)
-    if workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"the workspace must have at least {need} bytes")
-    d = gdn_attn_desc(batch, heads, rows, _row_stride(q, heads, dim, "q"), width, int(window),
-                      dim ** -0.5 if scale is None else scale, 0)
-    _check(_fn("gdn_paged_attention")(
+        lse_ptr = lse_out.data_ptr()
+    need = _attention_bytes(c.dtype, dim, batch)
+    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"the workspace must be contiguous and have at least {need} bytes")
+    d = _attn_desc(batch, heads, rows, _row_stride(q_shape, q.stride(), "q"), width, int(window),
+                   dim ** -0.5 if scale is None else scale, 0)
+    status = _fn("gdn_paged_attention")(
         ctypes.byref(d), ctypes.byref(c), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-        cu_seqlens.data_ptr(), context_len.data_ptr(), o_out.data_ptr(), _ptr(lse_out), workspace.data_ptr(),
-        _launch_stream(stream, device)), "gdn_paged_attention")
+        cu_seqlens.data_ptr(), context_len.data_ptr(), o_out.data_ptr(), lse_ptr, workspace.data_ptr(),
+        _launch_stream(stream, device))
+    if status:
+        _check(status, "gdn_paged_attention")
 
 
 class _Plan:

@@ -103,7 +103,7 @@ enum HeadKind { kNone = -1, kQ, kK, kV };
 // Block: RT consecutive rows (blockIdx.x) and the heads of one of gridDim.y shares; the
 // lane groups are dealt to the rows, and each walks its row's share of the q, k and v heads.
 template <typename T, int D, int RT, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeArgs a) {
     using V = Vec16<T>;
     constexpr int N = V::N;
     constexpr int LPH = D / N;                  // lanes of one head
@@ -287,11 +287,15 @@ cudaError_t launch_rt(const NormRopeArgs& a, cudaStream_t stream) {
 }
 
 // One row per block while the rows are few, so that a row's heads spread over all lane
-// groups; eight rows per block otherwise: two angles a thread, and A and B last for twice
-// as many heads as with four (67001 rows: 160 against 190 us).
+// groups; eight rows per block otherwise, and one per lane group (at most 16) once that
+// still gives two blocks per SM: A and B then last for all heads of a row (67001 rows of 24
+// heads: 256, 203 and 187 us with 4, 8 and 16 rows).
 template <typename T, int D, bool IL>
 cudaError_t launch_rows(const NormRopeArgs& a, cudaStream_t stream) {
-    return a.rows <= 296 ? launch_rt<T, D, 1, IL>(a, stream) : launch_rt<T, D, 8, IL>(a, stream);
+    constexpr int GROUPS = kThreads / (D / Vec16<T>::N);
+    constexpr int MANY = GROUPS < 16 ? GROUPS : 16;
+    if (a.rows <= 296) return launch_rt<T, D, 1, IL>(a, stream);
+    return a.rows < 296 * MANY ? launch_rt<T, D, 8, IL>(a, stream) : launch_rt<T, D, MANY, IL>(a, stream);
 }
 
 template <typename T, int D>
