@@ -77,14 +77,21 @@ __global__ void __launch_bounds__(1024) line_kernel(const Args a) {
 // columns 4 tx + 64 j.  K of the next tile is copied (cp.async) while P V runs, V while
 // the scores do; 113 KB for d = 128, so that two CTAs share an SM.  Bound by the fp32 pipe
 // (4 d flops per row and key).
-constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+//
+// Units of at most 8 rows (single tokens) would leave most of those tiles empty and seven
+// warps idle; they have all threads on the keys: four lanes per key for the scores, a warp
+// per row for the softmax, and for P V a thread per column and share of the keys.  Bound by
+// HBM then.
+constexpr int kRows = 64, kKeys = 64, kThreads = 256, kFew = 8;
 
 template <int D>
 struct SimtSmem {
     float q[kRows][D];
     float k[kKeys][D + 4];                         // padded: float4 reads of 8 rows hit 32 banks
     float v[kKeys][D];
-    float p[kRows][kKeys];
+    float p[kRows][kKeys];                         // few rows: [8][64] and behind them
+    __device__ float* keep() { return p[kFew]; }   // 2^(old maximum - new) of each row
+    __device__ float* inv() { return p[kFew + 1]; }
 };
 
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
@@ -153,126 +160,225 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
         }
         copy_rows(a.k, &sm.k[0][0], D + 4, (u.r.tile0 + kt0) * kKeys);
         copies_commit();
-        float m[4], l[4], o[4][D / 16];
-        int top_key[4], low_key[4];                // keys [low, top] are seen
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.0f;
-            top_key[i] = first_pos + (4 * ty + i) / a.group;
-            low_key[i] = a.window > 0 ? max(0, top_key[i] - a.window + 1) : 0;
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) o[i][j] = 0.0f;
-        }
-        const bool active = (4 * (ty & ~1)) < rows;   // warp-uniform: some row of this warp is a real one
-        for (int kt = kt0; kt < kt1; ++kt) {
-            const int key0 = (u.r.tile0 + kt) * kKeys;
-            copy_rows(a.v, &sm.v[0][0], D, key0);     // its last readers passed the barrier below
-            copies_commit();
-            copies_wait<1>();
-            __syncthreads();                          // K (and Q) are in
-            float s[4][4];
-            if (active) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
-#pragma unroll 4
-                for (int c = 0; c < D; c += 4) {
-                    float4 qv[4], kv[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + i][c]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-                            s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-                            s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-                            s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float top = m[i];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int key = key0 + tx + 16 * j;
-                        s[i][j] = key >= low_key[i] && key <= top_key[i] ? s[i][j] * scale : -INFINITY;
-                        top = fmaxf(top, s[i][j]);
-                    }
-#pragma unroll
-                    for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const float ref = top == -INFINITY ? 0.0f : top;
-                    const float keep = exp2f(m[i] - ref);
-                    m[i] = top;
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        s[i][j] = exp2f(s[i][j] - ref);
-                        sum += s[i][j];
-                        sm.p[4 * ty + i][tx + 16 * j] = s[i][j];
-                    }
-                    l[i] = l[i] * keep + sum;         // this lane's share of the row's sum
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) o[i][j] *= keep;
-                }
-            }
-            __syncthreads();                          // K is read
-            if (kt + 1 < kt1) copy_rows(a.k, &sm.k[0][0], D + 4, key0 + kKeys);
-            copies_commit();
-            copies_wait<1>();
-            __syncthreads();                          // V is in, P is written
-            if (active) {
-#pragma unroll 2
-                for (int c = 0; c < kKeys; c += 4) {
-                    float4 pv[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(&sm.p[4 * ty + i][c]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int j = 0; j < D / 64; ++j) {
-                            const float4 x = *reinterpret_cast<const float4*>(&sm.v[c + e][4 * tx + 64 * j]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float p = e == 0 ? pv[i].x : e == 1 ? pv[i].y : e == 2 ? pv[i].z : pv[i].w;
-                                o[i][4 * j] = fmaf(p, x.x, o[i][4 * j]);
-                                o[i][4 * j + 1] = fmaf(p, x.y, o[i][4 * j + 1]);
-                                o[i][4 * j + 2] = fmaf(p, x.z, o[i][4 * j + 2]);
-                                o[i][4 * j + 3] = fmaf(p, x.w, o[i][4 * j + 3]);
-                            }
-                        }
-                }
-            }
-            __syncthreads();                          // V and P are read
-        }
         const bool whole = kt0 == 0 && kt1 == u.r.tiles;
         auto out_row = [&](int r) {
             return (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.num_heads + u.head * a.group + r % a.group;
         };
-        if (active) {
+        if (rows <= kFew) {
+            const int lane = tid & 31, warp = tid >> 5;     // warp w has row w
+            const int top_key = first_pos + warp / a.group;
+            const int low_key = a.window > 0 ? max(0, top_key - a.window + 1) : 0;
+            constexpr int SHARES = kThreads / D;            // of the keys, for P V
+            const int col = tid % D, share = tid / D;
+            float m = -INFINITY, l = 0.0f, acc[kFew];
+#pragma unroll
+            for (int r = 0; r < kFew; ++r) acc[r] = 0.0f;
+            for (int kt = kt0; kt < kt1; ++kt) {
+                const int key0 = (u.r.tile0 + kt) * kKeys;
+                copy_rows(a.v, &sm.v[0][0], D, key0);
+                copies_commit();
+                copies_wait<1>();
+                __syncthreads();                            // K (and Q) are in
+                {
+                    const int key = tid >> 2, part = tid & 3;
+                    float sc[kFew];
+#pragma unroll
+                    for (int r = 0; r < kFew; ++r) sc[r] = 0.0f;
+#pragma unroll 4
+                    for (int c = 4 * part; c < D; c += 16) {
+                        const float4 kv = *reinterpret_cast<const float4*>(&sm.k[key][c]);
+#pragma unroll
+                        for (int r = 0; r < kFew; ++r)
+                            if (r < rows) {
+                                const float4 qv = *reinterpret_cast<const float4*>(&sm.q[r][c]);
+                                sc[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, sc[r]))));
+                            }
+                    }
+#pragma unroll
+                    for (int r = 0; r < kFew; ++r) {
+                        sc[r] += __shfl_xor_sync(0xffffffffu, sc[r], 1);
+                        sc[r] += __shfl_xor_sync(0xffffffffu, sc[r], 2);
+                        if ((r & 3) == part) sm.p[r][key] = sc[r] * scale;
+                    }
+                }
+                __syncthreads();                            // the scores are in, K is read
+                if (kt + 1 < kt1) copy_rows(a.k, &sm.k[0][0], D + 4, key0 + kKeys);
+                copies_commit();
+                if (warp < rows) {
+                    float s0 = sm.p[warp][lane], s1 = sm.p[warp][lane + 32];
+                    const int k0 = key0 + lane, k1 = k0 + 32;
+                    s0 = k0 >= low_key && k0 <= top_key ? s0 : -INFINITY;
+                    s1 = k1 >= low_key && k1 <= top_key ? s1 : -INFINITY;
+                    float top = fmaxf(m, fmaxf(s0, s1));
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const float ref = top == -INFINITY ? 0.0f : top;
+                    const float keep = exp2f(m - ref), p0 = exp2f(s0 - ref), p1 = exp2f(s1 - ref);
+                    m = top;
+                    l = l * keep + (p0 + p1);               // this lane's share of the row's sum
+                    sm.p[warp][lane] = p0;
+                    sm.p[warp][lane + 32] = p1;
+                    if (lane == 0) sm.keep()[warp] = keep;
+                }
+                copies_wait<1>();
+                __syncthreads();                            // V and P are in
+#pragma unroll
+                for (int r = 0; r < kFew; ++r)
+                    if (r < rows) acc[r] *= sm.keep()[r];
+#pragma unroll 2
+                for (int key = share * (kKeys / SHARES); key < (share + 1) * (kKeys / SHARES); key += 4) {
+                    const float v0 = sm.v[key][col], v1 = sm.v[key + 1][col], v2 = sm.v[key + 2][col],
+                                v3 = sm.v[key + 3][col];
+#pragma unroll
+                    for (int r = 0; r < kFew; ++r)
+                        if (r < rows) {
+                            const float4 pv = *reinterpret_cast<const float4*>(&sm.p[r][key]);
+                            acc[r] = fmaf(pv.x, v0, fmaf(pv.y, v1, fmaf(pv.z, v2, fmaf(pv.w, v3, acc[r]))));
+                        }
+                }
+                __syncthreads();                            // V and P are read
+            }
+            // the shares of the keys join in the K buffer
+            float* part = &sm.k[0][0];
+#pragma unroll
+            for (int r = 0; r < kFew; ++r) part[(share * kFew + r) * D + col] = acc[r];
+            if (warp < rows) {
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+                if (lane == 0) {
+                    const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+                    sm.inv()[warp] = l == 0.0f ? 0.0f : 1.0f / l;
+                    if (!whole) a.part_lse[part_slot(blockIdx.x, begins) * kRows + warp] = lse2;
+                    else if (a.lse) a.lse[out_row(warp)] = lse2 * kLn2;
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < rows * D; i += kThreads) {
+                const int r = i / D, c = i % D;
+                float x = 0.0f;
+#pragma unroll
+                for (int n = 0; n < SHARES; ++n) x += part[(n * kFew + r) * D + c];
+                (whole ? static_cast<float*>(a.o) + out_row(r) * D
+                       : a.part_o + (part_slot(blockIdx.x, begins) * kRows + r) * D)[c] = x * sm.inv()[r];
+            }
+        } else {
+            float m[4], l[4], o[4][D / 16];
+            int top_key[4], low_key[4];                // keys [low, top] are seen
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float sum = l[i];
+                m[i] = -INFINITY;
+                l[i] = 0.0f;
+                top_key[i] = first_pos + (4 * ty + i) / a.group;
+                low_key[i] = a.window > 0 ? max(0, top_key[i] - a.window + 1) : 0;
 #pragma unroll
-                for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const float lse2 = sum == 0.0f ? -INFINITY : m[i] + log2f(sum);
-                const int r = 4 * ty + i;
-                if (r >= rows) continue;
-                const long long orow = out_row(r), prow = part_slot(blockIdx.x, begins) * kRows + r;
+                for (int j = 0; j < D / 16; ++j) o[i][j] = 0.0f;
+            }
+            const bool active = (4 * (ty & ~1)) < rows;   // warp-uniform: some row of this warp is a real one
+            for (int kt = kt0; kt < kt1; ++kt) {
+                const int key0 = (u.r.tile0 + kt) * kKeys;
+                copy_rows(a.v, &sm.v[0][0], D, key0);     // its last readers passed the barrier below
+                copies_commit();
+                copies_wait<1>();
+                __syncthreads();                          // K (and Q) are in
+                float s[4][4];
+                if (active) {
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j)
-                    *reinterpret_cast<float4*>((whole ? static_cast<float*>(a.o) + orow * D : a.part_o + prow * D) +
-                                               4 * tx + 64 * j) =
-                        make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
-                                    o[i][4 * j + 3] * inv);
-                if (tx == 0) {
-                    if (!whole) a.part_lse[prow] = lse2;
-                    else if (a.lse) a.lse[orow] = lse2 * kLn2;
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+#pragma unroll 4
+                    for (int c = 0; c < D; c += 4) {
+                        float4 qv[4], kv[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + i][c]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+                                s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+                                s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+                                s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float top = m[i];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = key0 + tx + 16 * j;
+                            s[i][j] = key >= low_key[i] && key <= top_key[i] ? s[i][j] * scale : -INFINITY;
+                            top = fmaxf(top, s[i][j]);
+                        }
+#pragma unroll
+                        for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const float ref = top == -INFINITY ? 0.0f : top;
+                        const float keep = exp2f(m[i] - ref);
+                        m[i] = top;
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            s[i][j] = exp2f(s[i][j] - ref);
+                            sum += s[i][j];
+                            sm.p[4 * ty + i][tx + 16 * j] = s[i][j];
+                        }
+                        l[i] = l[i] * keep + sum;         // this lane's share of the row's sum
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) o[i][j] *= keep;
+                    }
+                }
+                __syncthreads();                          // K is read
+                if (kt + 1 < kt1) copy_rows(a.k, &sm.k[0][0], D + 4, key0 + kKeys);
+                copies_commit();
+                copies_wait<1>();
+                __syncthreads();                          // V is in, P is written
+                if (active) {
+#pragma unroll 2
+                    for (int c = 0; c < kKeys; c += 4) {
+                        float4 pv[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(&sm.p[4 * ty + i][c]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int j = 0; j < D / 64; ++j) {
+                                const float4 x = *reinterpret_cast<const float4*>(&sm.v[c + e][4 * tx + 64 * j]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float p = e == 0 ? pv[i].x : e == 1 ? pv[i].y : e == 2 ? pv[i].z : pv[i].w;
+                                    o[i][4 * j] = fmaf(p, x.x, o[i][4 * j]);
+                                    o[i][4 * j + 1] = fmaf(p, x.y, o[i][4 * j + 1]);
+                                    o[i][4 * j + 2] = fmaf(p, x.z, o[i][4 * j + 2]);
+                                    o[i][4 * j + 3] = fmaf(p, x.w, o[i][4 * j + 3]);
+                                }
+                            }
+                    }
+                }
+                __syncthreads();                          // V and P are read
+            }
+            if (active) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float sum = l[i];
+#pragma unroll
+                    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    const float lse2 = sum == 0.0f ? -INFINITY : m[i] + log2f(sum);
+                    const int r = 4 * ty + i;
+                    if (r >= rows) continue;
+                    const long long orow = out_row(r), prow = part_slot(blockIdx.x, begins) * kRows + r;
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j)
+                        *reinterpret_cast<float4*>((whole ? static_cast<float*>(a.o) + orow * D : a.part_o + prow * D) +
+                                                   4 * tx + 64 * j) =
+                            make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
+                                        o[i][4 * j + 3] * inv);
+                    if (tx == 0) {
+                        if (!whole) a.part_lse[prow] = lse2;
+                        else if (a.lse) a.lse[orow] = lse2 * kLn2;
+                    }
                 }
             }
         }

@@ -51,7 +51,6 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a row's maximum that P absorbs
 constexpr int kPoly = 5;           // of 16 pairs of exponentials, those on the FMA pipe (measured: 0 .. 8)
-constexpr int kMerge = 6;          // parts of a split unit read at once
 constexpr int kBlock = kKeys * 128;   // bytes of one 64-column block of a 128-row tile
 
 template <int D>
@@ -261,8 +260,6 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             p.single = u.r.toks <= a.block_tokens;
             p.slot = p.n == u.r.tiles ? -1 : (int)part_slot(blockIdx.x, i == 0);
             p.split = split_of(u, per);
-            if (p.slot >= 0 && lane < kArrivals) claim_arrivals(a, p.split, lane);
-            __syncwarp();
             pos += p.n;
         }
         if (lane == 0) {
@@ -466,6 +463,80 @@ __device__ __forceinline__ void mma_role(const Args& a, uint8_t* smem, Bars* b, 
     mbar_wait_bounded(&b->drain[s], 0, kWaitNs);
 }
 
+// ---------------------------------------------------------------- the merge
+// A warp's rows of a split unit merged from its parts: a lane has one row (lse_row of the
+// log-sums) and of its columns the groups of four first, first + step, ...; group g of a part
+// sits at offset + g * stride values in the part's slot.  The latency of the reads is most of
+// the cost, so PARTS parts of GROUPS groups are read at once, their log-sums beside them.
+template <int D>
+struct Merge {
+    const Args& a;
+    const Split& sp;
+    int lse_row;
+    long long offset;
+    int stride;
+    bool mine;                // the lane has a row
+    int groups, first, step;
+
+    template <int GROUPS, int PARTS>
+    __device__ __forceinline__ void run(__nv_bfloat16* to, float* lse_out) const {
+        for (int g0 = first; g0 < groups; g0 += GROUPS * step) {
+            float top = -INFINITY, sum = 0.0f;
+            float4 acc[GROUPS];
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) acc[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int p0 = sp.first; p0 <= sp.last; p0 += PARTS) {
+                float w[PARTS];
+                float4 y[PARTS][GROUPS];
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) {
+                    const bool on = mine && p0 + i <= sp.last;
+                    const long long slot = on ? sp.slot(p0 + i) : 0;
+                    w[i] = on ? __ldcg(a.part_lse + slot * (2 * kRows) + lse_row) : -INFINITY;
+                    const float* from = a.part_o + slot * (2 * kRows * D) + offset;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g)
+                        y[i][g] = on && g0 + g * step < groups
+                                      ? __ldcg(reinterpret_cast<const float4*>(from + (g0 + g * step) * stride))
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+                float t = top;
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) t = fmaxf(t, w[i]);
+                const float ref = t == -INFINITY ? 0.0f : t, keep = ex2(top - ref);
+                top = t;
+                sum *= keep;
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    acc[g].x *= keep;
+                    acc[g].y *= keep;
+                    acc[g].z *= keep;
+                    acc[g].w *= keep;
+                }
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) {
+                    const float f = ex2(w[i] - ref);
+                    sum += f;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        acc[g].x = fmaf(f, y[i][g].x, acc[g].x);
+                        acc[g].y = fmaf(f, y[i][g].y, acc[g].y);
+                        acc[g].z = fmaf(f, y[i][g].z, acc[g].z);
+                        acc[g].w = fmaf(f, y[i][g].w, acc[g].w);
+                    }
+                }
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a NaN part makes the row NaN
+            if (lse_out && g0 == 0) *lse_out = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+                if (mine && g0 + g * step < groups)
+                    *reinterpret_cast<uint2*>(to + 4 * (g0 + g * step)) =
+                        make_uint2(pack(acc[g].x * inv, acc[g].y * inv), pack(acc[g].z * inv, acc[g].w * inv));
+        }
+    }
+};
+
 // ------------------------------------------------------------ softmax groups
 template <int D>
 __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars* b, int s) {
@@ -476,6 +547,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
     const uint32_t tm_o = tm + 256 + s * 128;
     float* exch = reinterpret_cast<float*>(smem + S::EXCH);
     const float sl = a.scale * 1.4426950408889634f;
+    const int row_tok = row / a.group, row_head = row % a.group;   // of a row tile's rows
     unsigned steps = 0, x_count = 0;   // steps of this stream, over all pieces
     bool ok = true;
     Pieces pieces;
@@ -484,12 +556,15 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         const int toks = min(a.block_tokens, u.toks - sub * a.block_tokens);
         const int rows = toks * a.group;
         const int first_pos = u.first_pos + sub * a.block_tokens;
-        const int top_key = row < rows ? first_pos + row / a.group : -1;     // keys [low_key, top_key] are seen
+        const int top_key = row < rows ? first_pos + row_tok : -1;     // keys [low_key, top_key] are seen
         const int low_key = a.window > 0 ? max(0, top_key - a.window + 1) : 0;
         // keys that every row of the tile sees: [all_lo, all_hi]
         const int all_hi = first_pos;
         const int all_lo = a.window > 0 ? max(0, first_pos + toks - a.window) : 0;
         const bool active = quarter * 32 < rows;   // this warp has rows
+        // while the first scores are on their way
+        if (active && u.slot >= 0 && lane == 0) claim_arrivals(a, u.split, s * 4 + quarter);
+        __syncwarp();
         float m = -INFINITY;
         const Pair scale = pair(sl, sl);
         Pair sum[2] = {0ull, 0ull};
@@ -570,9 +645,8 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
             if (!ok) break;
         }
         tc_fence_after();
-        const int h = row % a.group;
         const long long orow =
-            (long long)(u.row0 + sub * a.block_tokens + row / a.group) * a.num_heads + u.head * a.group + h;
+            (long long)(u.row0 + sub * a.block_tokens + row_tok) * a.num_heads + u.head * a.group + row_head;
         const bool whole = u.slot < 0;
         // Partial outputs of this warp's rows (single: of this group's half of their columns):
         // [columns / 4][R] float4 with R the rows of the warp, rounded up to a power of two, so
@@ -633,58 +707,19 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
             }
             if (!whole) {
                 // the warp that brings the last part of its rows (single: of its half of their
-                // columns) merges them: lane -> row lane % R and columns 4 (lane / R), 4 (lane / R
-                // + 32 / R), ...; kMerge reads of each of four column groups at once
+                // columns) merges them
                 __threadfence();
                 __syncwarp();
                 const bool last = __shfl_sync(0xffffffffu, lane == 0 && arrive_last(a, u.split, s * 4 + quarter), 0);
                 if (last) {
                     const int r = lane & (R - 1), at = quarter * 32 + r;
-                    const bool mine = at < rows;
-                    RowMerge rm{0.0f, 0.0f, 0.0f};
-                    if (mine) rm = merge_row(a, u.split, s * kRows + at);
-                    const long long to = ((long long)(u.row0 + sub * a.block_tokens + at / a.group) * a.num_heads +
-                                          u.head * a.group + at % a.group) * D + (u.single ? s * (D / 2) : 0);
-                    if (a.lse && mine && lane < R && (!u.single || s == 0)) a.lse[to / D] = rm.lse * kLn2;
-                    const int groups = (u.single ? D / 2 : D) / 4, step = 32 >> log_r;
-                    for (int g0 = lane >> log_r; g0 < groups; g0 += 4 * step) {
-                        float4 acc[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) acc[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        for (int p0 = u.split.first; p0 <= u.split.last; p0 += kMerge) {
-                            float w[kMerge];
-                            float4 y[kMerge][4];
-#pragma unroll
-                            for (int i = 0; i < kMerge; ++i) {
-                                const bool on = mine && p0 + i <= u.split.last;
-                                const long long slot = on ? u.split.slot(p0 + i) : 0;
-                                w[i] = on ? __ldcg(a.part_lse + slot * (2 * kRows) + s * kRows + at) : -INFINITY;
-                                const float4* from =
-                                    reinterpret_cast<const float4*>(a.part_o + slot * (2 * kRows * D) + warp_at) + r;
-#pragma unroll
-                                for (int g = 0; g < 4; ++g)
-                                    y[i][g] = on && g0 + g * step < groups ? __ldcg(from + (g0 + g * step) * R)
-                                                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            }
-#pragma unroll
-                            for (int i = 0; i < kMerge; ++i) {
-                                const float f = ex2(w[i] - rm.top);
-#pragma unroll
-                                for (int g = 0; g < 4; ++g) {
-                                    acc[g].x = fmaf(f, y[i][g].x, acc[g].x);
-                                    acc[g].y = fmaf(f, y[i][g].y, acc[g].y);
-                                    acc[g].z = fmaf(f, y[i][g].z, acc[g].z);
-                                    acc[g].w = fmaf(f, y[i][g].w, acc[g].w);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (mine && g0 + g * step < groups)
-                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + to + 4 * (g0 + g * step)) =
-                                    make_uint2(pack(acc[g].x * rm.inv, acc[g].y * rm.inv),
-                                               pack(acc[g].z * rm.inv, acc[g].w * rm.inv));
-                    }
+                    const long long orow_r = __shfl_sync(0xffffffffu, orow, r);
+                    const Merge<D> mg{a, u.split, s * kRows + at, warp_at + 4 * r, 4 * R, at < rows,
+                                      u.single ? D / 8 : D / 4, lane >> log_r, 32 >> log_r};
+                    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.o) + orow_r * D + (u.single ? s * (D / 2) : 0);
+                    float* lse = a.lse && at < rows && lane < R && (!u.single || s == 0) ? a.lse + orow_r : nullptr;
+                    if (u.split.last - u.split.first < 3) mg.template run<8, 3>(to, lse);
+                    else mg.template run<4, 6>(to, lse);
                 }
             }
         }
