@@ -685,6 +685,7 @@ gdn_status gdn_paged_attention(const gdn_attn_desc* d, const gdn_paged_kv* cache
     a.line = reinterpret_cast<gdn::attn::Line*>(w + lay.line);
     a.seqs = reinterpret_cast<gdn::attn::Seq*>(w + lay.seqs);
     a.arrivals = reinterpret_cast<unsigned long long*>(w + lay.arrivals);
+    a.splits = reinterpret_cast<gdn::attn::SplitUnit*>(w + lay.splits);
     a.part_lse = reinterpret_cast<float*>(w + lay.part_lse);
     a.part_o = reinterpret_cast<float*>(w + lay.part_o);
     if (gdn::launch_paged_attention(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {

@@ -469,7 +469,8 @@ attn::Layout paged_attention_layout(int dtype, int dim, int batch) {
     l.line = sizeof(WorkspaceHeader);
     l.seqs = l.line + sizeof(attn::Line);
     l.arrivals = l.seqs + up(sizeof(attn::Seq) * (size_t)batch);
-    l.part_lse = l.arrivals + up(sizeof(unsigned long long) * (size_t)sh.max_parts * attn::kArrivals);
+    l.splits = l.arrivals + up(sizeof(unsigned long long) * (size_t)sh.max_parts * attn::kArrivals);
+    l.part_lse = l.splits + up(sizeof(attn::SplitUnit) * (size_t)sh.max_parts);
     l.part_o = l.part_lse + up(sizeof(float) * rows);
     l.bytes = l.part_o + up(sizeof(float) * rows * dim);
     return l;
@@ -482,6 +483,7 @@ cudaError_t launch_paged_attention(const attn::Args& args, cudaStream_t stream) 
     const long long step = (long long)a.block_tokens * a.shape.subs;
     a.line_inline = a.batch <= a.shape.threads && (a.rows + step - 1) / step <= 32;
     if (a.line_inline && a.batch <= 32 && a.dtype == GDN_BF16) a.line_inline = 2;   // no block barrier before the first loads
+    a.merge_kernel = a.shape.subs > 1 && a.rows > a.block_tokens;
     if (!a.line_inline) {
         attn::line_kernel<<<1, 1024, 0, stream>>>(a);
         const cudaError_t e = cudaGetLastError();

@@ -10,7 +10,8 @@
 // GPU.  A CTA that holds a unit whole writes its outputs.  A unit that the cuts split
 // leaves normalised partial outputs and log-sums; whoever brings the last part of some
 // rows merges all of them, in the order of the line, so the result does not depend on
-// which CTA that was.  (A merging kernel of its own took 10 to 35 us a call.)
+// which CTA that was.  Units of two row tiles (bf16) are merged by a kernel of their own,
+// over all SMs: their parts, up to 128 KB each, took the last CTA 12 to 15 us.
 //
 // The lengths are read on the device (a captured call may be replayed with new ones).
 // When the sequences and their token blocks are few, every CTA lays out the line for
@@ -47,6 +48,16 @@ struct Line {
 };
 static_assert(sizeof(Line) == 256, "Line is 256 bytes");
 
+// A unit of two row tiles that begins in CTA i and ends in a later one, for the merging
+// kernel: slot i of a table that every CTA writes.
+struct SplitUnit {
+    int last;            // its last part; -1 = there is no such unit
+    int from_start;      // it begins where CTA i's stretch does
+    int row0, toks, head;
+    int pad[3];
+};
+static_assert(sizeof(SplitUnit) == 32, "SplitUnit is 32 bytes");
+
 // Sizes that a kernel family fixes.
 struct Shape {
     int sub_rows;        // rows of one row tile
@@ -81,6 +92,8 @@ struct Args {
     Line* line;
     Seq* seqs;                              // [batch]
     unsigned long long* arrivals;           // [max_parts * kArrivals]: parts of split units that are in
+    int merge_kernel;                       // there may be units of two row tiles
+    SplitUnit* splits;                      // [max_parts]
     float* part_lse;                        // [2 * max_parts][subs * sub_rows], base 2
     float* part_o;                          // [2 * max_parts] slots of subs * sub_rows * dim values
 };
@@ -393,7 +406,7 @@ Shape shape_tc();
 // Byte offsets of a call's workspace: status header, line, sequences, partial results.
 namespace attn {
 struct Layout {
-    size_t line, seqs, arrivals, part_lse, part_o, bytes;
+    size_t line, seqs, arrivals, splits, part_lse, part_o, bytes;
 };
 }  // namespace attn
 

@@ -244,8 +244,7 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
     last.n = 0;
     for (unsigned i = 0;; ++i) {
         if (i >= 2 && !wait(b, &b->piece_free[i & 1], (i / 2 - 1) & 1)) return;
-        Piece p;
-        p.n = 0;
+        Piece p{};
         if (pos < end) {
             const int kt0 = (int)(pos - u.begin), kt1 = (int)min((long long)u.r.tiles, end - u.begin);
             p.n = kt1 - kt0;
@@ -267,6 +266,11 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             mbar_arrive(&b->piece_full[i & 1]);
         }
         __syncwarp();
+        if (a.merge_kernel && lane == 0 && pos >= end && (p.n > 0 || i == 0)) {   // the stretch's last piece
+            const bool goes_on = p.n > 0 && !p.single && p.slot >= 0 && p.split.first == (int)blockIdx.x &&
+                                 p.split.last > p.split.first;
+            a.splits[blockIdx.x] = SplitUnit{goes_on ? p.split.last : -1, p.split.from_start, p.row0, p.toks, p.head, {}};
+        }
         for (int j = 0; j < last.n; ++j, ++tiles) {
             if (!last.ragged(j)) continue;
             const int from = last.from(j), to = last.to(j);
@@ -563,7 +567,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         const int all_lo = a.window > 0 ? max(0, first_pos + toks - a.window) : 0;
         const bool active = quarter * 32 < rows;   // this warp has rows
         // while the first scores are on their way
-        if (active && u.slot >= 0 && lane == 0) claim_arrivals(a, u.split, s * 4 + quarter);
+        if (active && u.slot >= 0 && u.single && lane == 0) claim_arrivals(a, u.split, s * 4 + quarter);
         __syncwarp();
         float m = -INFINITY;
         const Pair scale = pair(sl, sl);
@@ -705,9 +709,8 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                 if (!whole) a.part_lse[(long long)u.slot * (2 * kRows) + s * kRows + row] = lse2;
                 else if (a.lse && (!u.single || s == 0)) a.lse[orow] = lse2 * kLn2;
             }
-            if (!whole) {
-                // the warp that brings the last part of its rows (single: of its half of their
-                // columns) merges them
+            if (!whole && u.single) {
+                // the warp that brings the last part of its half of its rows' columns merges them
                 __threadfence();
                 __syncwarp();
                 const bool last = __shfl_sync(0xffffffffu, lane == 0 && arrive_last(a, u.split, s * 4 + quarter), 0);
@@ -715,11 +718,10 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                     const int r = lane & (R - 1), at = quarter * 32 + r;
                     const long long orow_r = __shfl_sync(0xffffffffu, orow, r);
                     const Merge<D> mg{a, u.split, s * kRows + at, warp_at + 4 * r, 4 * R, at < rows,
-                                      u.single ? D / 8 : D / 4, lane >> log_r, 32 >> log_r};
-                    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.o) + orow_r * D + (u.single ? s * (D / 2) : 0);
-                    float* lse = a.lse && at < rows && lane < R && (!u.single || s == 0) ? a.lse + orow_r : nullptr;
-                    if (u.split.last - u.split.first < 3) mg.template run<8, 3>(to, lse);
-                    else mg.template run<4, 6>(to, lse);
+                                      D / 8, lane >> log_r, 32 >> log_r};
+                    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.o) + orow_r * D + s * (D / 2);
+                    float* lse = a.lse && at < rows && lane < R && s == 0 ? a.lse + orow_r : nullptr;
+                    mg.template run<4, 6>(to, lse);
                 }
             }
         }
@@ -744,7 +746,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Line ln;
     if (a.line_inline != 2) {
         ln = get_line<kThreads>(a, reinterpret_cast<long long*>(smem + S::SCAN));
-        if ((int)blockIdx.x >= ln.parts) return;
+        if ((int)blockIdx.x >= ln.parts) {
+            if (a.merge_kernel && threadIdx.x == 0) a.splits[blockIdx.x].last = -1;
+            return;
+        }
     } else if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.ws->epoch = a.epoch;
     }
@@ -788,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) {
         softmax_role<D>(a, smem, b, warp >> 2);
     } else if (warp < 10) {
@@ -814,6 +820,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// The units of two row tiles that the cuts split, each by its parts in the order of the
+// line: block (i, share) the unit that CTA i of the attention kernel began, 32 rows of it, the
+// columns over eight warps.  23 MB of parts read once by all SMs; launched so that its blocks
+// start as the attention kernel's leave (programmatic dependent launch) and wait for the
+// rest of them.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const Args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const SplitUnit u = a.splits[blockIdx.x];
+    if (u.last < 0) return;
+    const int s = blockIdx.y >> 2, quarter = blockIdx.y & 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = min(a.block_tokens, u.toks - s * a.block_tokens) * a.group;
+    const int warp_rows = min(32, rows - quarter * 32);
+    if (warp_rows <= 0) return;
+    const int log_r = warp_rows <= 1 ? 0 : 32 - __clz(warp_rows - 1), R = 1 << log_r;
+    const int r = lane & (R - 1), at = quarter * 32 + r;
+    const long long row = (long long)(u.row0 + s * a.block_tokens + at / a.group) * a.num_heads + u.head * a.group +
+                          at % a.group;
+    const Split sp{(int)blockIdx.x, u.last, u.from_start != 0};
+    const int step = 32 >> log_r;
+    const Merge<D> mg{a, sp, s * kRows + at, (long long)(s * 4 + quarter) * 32 * D + 4 * r, 4 * R, at < rows,
+                      D / 4, (lane >> log_r) + warp * step, 8 * step};
+    float* lse = a.lse && at < rows && lane < R && warp == 0 ? a.lse + row : nullptr;
+    mg.template run<4, 6>(static_cast<__nv_bfloat16*>(a.o) + row * D, lse);
+}
+
 bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
             const cuuint32_t* box) {
     const cuuint32_t es[4] = {1, 1, 1, 1};
@@ -830,7 +862,18 @@ cudaError_t launch_typed(const Args& a, const Maps& maps, int granule, cudaStrea
         ensure_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<D>), Smem<D>::BYTES, smem_set);
     if (e != cudaSuccess) return e;
     attn_tc_kernel<D><<<kMaxParts, kThreads, Smem<D>::BYTES, stream>>>(a, maps, granule);
-    return cudaGetLastError();
+    const cudaError_t launched = cudaGetLastError();
+    if (launched != cudaSuccess || !a.merge_kernel) return launched;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kMaxParts - 1, 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, merge_kernel<D>, a);
 }
 
 }  // namespace
