@@ -727,7 +727,8 @@ class PagedAttention:
         n = gdn_paged_attention_workspace_bytes(dtype, head_dim, max_batch)
         if n == 0 or num_kv_heads < 1 or num_heads < 1 or num_heads % num_kv_heads:
             raise GdnError(GDN_ERR_UNSUPPORTED, "PagedAttention")
-        self.workspace = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
+        self.workspace[:256].zero_()   # the status, for status() before the first run
 
     def run(self, q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out=None, scale=None, window=0,
             stream=None, workspace=None):

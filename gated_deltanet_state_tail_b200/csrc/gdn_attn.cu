@@ -72,26 +72,30 @@ __global__ void __launch_bounds__(1024) line_kernel(const Args a) {
 }
 
 // ------------------------------------------------------------- fp32 attention
-// 64 rows x 64 keys per tile on the CUDA cores.  256 threads: thread (ty, tx) holds the
-// scores of rows 4 ty .. 4 ty + 3 and keys tx + 16 j, and the outputs of those rows and
-// columns 4 tx + 64 j.  K of the next tile is copied (cp.async) while P V runs, V while
-// the scores do; 113 KB for d = 128, so that two CTAs share an SM.  Bound by the fp32 pipe
-// (4 d flops per row and key).
+// 64 rows x 64 keys per tile on the CUDA cores.  128 threads: thread (ty, tx) holds the
+// scores of rows 8 ty .. 8 ty + 7 and keys tx + 16 j, and the outputs of those rows and
+// columns 4 tx + 64 j, so that 12 reads of shared memory feed 128 multiply-adds (with 4 x 4
+// scores a thread and 256 threads, 8 fed 64).  K of the next tile is copied (cp.async)
+// while P V runs, V while the scores do; 113 KB for d = 128, so that two CTAs share an SM.
+// The rows' places in the pages are worked out once per tile, a thread per row, and kept in
+// the padding of K's rows.  Bound by the fp32 pipe (4 d flops per row and key).
 //
-// Units of at most 8 rows (single tokens) would leave most of those tiles empty and seven
-// warps idle; they have all threads on the keys: four lanes per key for the scores, a warp
-// per row for the softmax, and for P V a thread per column and share of the keys.  Bound by
-// HBM then.
-constexpr int kRows = 64, kKeys = 64, kThreads = 256, kFew = 8;
-
+// Units of at most 8 rows (single tokens) would leave most of those tiles empty; they have
+// all threads on the keys: two lanes per key for the scores, a warp per two rows for the
+// softmax, and for P V a thread per column and share of the keys.  Bound by HBM then.
+constexpr int kRows = 64, kKeys = 64, kThreads = 128, kFew = 8;
+constexpr int kWarps = kThreads / 32, kTR = kRows / (kThreads / 16);   // kTR: rows of a thread
 template <int D>
 struct SimtSmem {
     float q[kRows][D];
-    float k[kKeys][D + 4];                         // padded: float4 reads of 8 rows hit 32 banks
+    // padded: float4 reads of 8 rows hit 32 banks; the padding holds two places in the
+    // pages, of this tile's row and of the next one's
+    float k[kKeys][D + 4];
     float v[kKeys][D];
     float p[kRows][kKeys];                         // few rows: [8][64] and behind them
     __device__ float* keep() { return p[kFew]; }   // 2^(old maximum - new) of each row
     __device__ float* inv() { return p[kFew + 1]; }
+    __device__ long long& place(int r, int slot) { return *reinterpret_cast<long long*>(&k[r][D + 2 * slot]); }
 };
 
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
@@ -124,28 +128,32 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
         const int kt1 = (int)min((long long)u.r.tiles, end - u.begin);
         const int rows = u.r.toks * a.group;
         const int first_pos = u.s.ctx - u.s.qlen + u.r.tok0;
-        // 64 rows of K or V, zero outside the unit's keys: a warp's lanes share a row
-        // (d = 128) or two, and so a page
-        auto copy_rows = [&](const void* base, float* dst, int ld, int key0) {
-#pragma unroll
+        // where the rows of the tile at key0 are in the pools; -1 outside the unit's keys and
+        // for a bad page number, both of which read as zeros
+        auto find_places = [&](int key0, int slot) {
+            if (tid >= kKeys) return;
+            const int key = key0 + tid;
+            long long at = -1;
+            if (key >= u.r.lo && key < u.r.hi) {
+                const int page = a.page_table[(long long)u.b * a.max_pages + key / a.page_size];
+                if (page >= 0 && page < a.num_pages)
+                    at = (long long)page * a.page_stride + (long long)(key % a.page_size) * a.row_stride +
+                         (long long)u.head * a.head_stride;
+                else
+                    report(a, kStatusMismatch);
+            }
+            sm.place(tid, slot) = at;
+        };
+        auto copy_rows = [&](const void* base, float* dst, int ld, int slot) {
+#pragma unroll 8
             for (int n = 0; n < kKeys * (D / 4) / kThreads; ++n) {
                 const int i = tid + n * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
-                const int key = key0 + r;
-                const float* src = static_cast<const float*>(base);
-                bool on = key >= u.r.lo && key < u.r.hi;
-                if (on) {
-                    const int page = a.page_table[(long long)u.b * a.max_pages + key / a.page_size];
-                    on = page >= 0 && page < a.num_pages;
-                    if (on)
-                        src += (long long)page * a.page_stride + (long long)(key % a.page_size) * a.row_stride +
-                               (long long)u.head * a.head_stride + c;
-                    else if (c == 0)
-                        report(a, kStatusMismatch);
-                }
-                copy16(dst + r * ld + c, src, on);
+                const long long at = sm.place(r, slot);
+                copy16(dst + r * ld + c, static_cast<const float*>(base) + (at >= 0 ? at + c : 0), at >= 0);
             }
         };
         __syncthreads();   // the last unit's reads of shared memory are over
+        find_places((u.r.tile0 + kt0) * kKeys, 0);
         // queries and the first tile's keys
 #pragma unroll
         for (int n = 0; n < kRows * (D / 4) / kThreads; ++n) {
@@ -158,34 +166,37 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                            : 0),
                    on);
         }
-        copy_rows(a.k, &sm.k[0][0], D + 4, (u.r.tile0 + kt0) * kKeys);
+        __syncthreads();   // the places are in
+        copy_rows(a.k, &sm.k[0][0], D + 4, 0);
         copies_commit();
         const bool whole = kt0 == 0 && kt1 == u.r.tiles;
         auto out_row = [&](int r) {
             return (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.num_heads + u.head * a.group + r % a.group;
         };
         if (rows <= kFew) {
-            const int lane = tid & 31, warp = tid >> 5;     // warp w has row w
-            const int top_key = first_pos + warp / a.group;
-            const int low_key = a.window > 0 ? max(0, top_key - a.window + 1) : 0;
+            const int lane = tid & 31, warp = tid >> 5;     // warp w has rows w and w + kWarps
+            constexpr int PARTS = kThreads / kKeys;         // lanes of a key, for the scores
             constexpr int SHARES = kThreads / D;            // of the keys, for P V
             const int col = tid % D, share = tid / D;
-            float m = -INFINITY, l = 0.0f, acc[kFew];
+            float m[kFew / kWarps], l[kFew / kWarps], acc[kFew];
+#pragma unroll
+            for (int j = 0; j < kFew / kWarps; ++j) m[j] = -INFINITY, l[j] = 0.0f;
 #pragma unroll
             for (int r = 0; r < kFew; ++r) acc[r] = 0.0f;
             for (int kt = kt0; kt < kt1; ++kt) {
-                const int key0 = (u.r.tile0 + kt) * kKeys;
-                copy_rows(a.v, &sm.v[0][0], D, key0);
+                const int key0 = (u.r.tile0 + kt) * kKeys, slot = (kt - kt0) & 1;
+                copy_rows(a.v, &sm.v[0][0], D, slot);
                 copies_commit();
+                if (kt + 1 < kt1) find_places(key0 + kKeys, slot ^ 1);
                 copies_wait<1>();
                 __syncthreads();                            // K (and Q) are in
                 {
-                    const int key = tid >> 2, part = tid & 3;
+                    const int key = tid / PARTS, part = tid % PARTS;
                     float sc[kFew];
 #pragma unroll
                     for (int r = 0; r < kFew; ++r) sc[r] = 0.0f;
 #pragma unroll 4
-                    for (int c = 4 * part; c < D; c += 16) {
+                    for (int c = 4 * part; c < D; c += 4 * PARTS) {
                         const float4 kv = *reinterpret_cast<const float4*>(&sm.k[key][c]);
 #pragma unroll
                         for (int r = 0; r < kFew; ++r)
@@ -196,29 +207,34 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                     }
 #pragma unroll
                     for (int r = 0; r < kFew; ++r) {
-                        sc[r] += __shfl_xor_sync(0xffffffffu, sc[r], 1);
-                        sc[r] += __shfl_xor_sync(0xffffffffu, sc[r], 2);
-                        if ((r & 3) == part) sm.p[r][key] = sc[r] * scale;
+#pragma unroll
+                        for (int d = PARTS / 2; d > 0; d >>= 1) sc[r] += __shfl_xor_sync(0xffffffffu, sc[r], d);
+                        if (r % PARTS == part) sm.p[r][key] = sc[r] * scale;
                     }
                 }
                 __syncthreads();                            // the scores are in, K is read
-                if (kt + 1 < kt1) copy_rows(a.k, &sm.k[0][0], D + 4, key0 + kKeys);
+                if (kt + 1 < kt1) copy_rows(a.k, &sm.k[0][0], D + 4, slot ^ 1);
                 copies_commit();
-                if (warp < rows) {
-                    float s0 = sm.p[warp][lane], s1 = sm.p[warp][lane + 32];
+#pragma unroll
+                for (int j = 0; j < kFew / kWarps; ++j) {
+                    const int r = warp + j * kWarps;
+                    if (r >= rows) break;
+                    const int top_key = first_pos + r / a.group;
+                    const int low_key = a.window > 0 ? max(0, top_key - a.window + 1) : 0;
+                    float s0 = sm.p[r][lane], s1 = sm.p[r][lane + 32];
                     const int k0 = key0 + lane, k1 = k0 + 32;
                     s0 = k0 >= low_key && k0 <= top_key ? s0 : -INFINITY;
                     s1 = k1 >= low_key && k1 <= top_key ? s1 : -INFINITY;
-                    float top = fmaxf(m, fmaxf(s0, s1));
+                    float top = fmaxf(m[j], fmaxf(s0, s1));
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                     const float ref = top == -INFINITY ? 0.0f : top;
-                    const float keep = exp2f(m - ref), p0 = exp2f(s0 - ref), p1 = exp2f(s1 - ref);
-                    m = top;
-                    l = l * keep + (p0 + p1);               // this lane's share of the row's sum
-                    sm.p[warp][lane] = p0;
-                    sm.p[warp][lane + 32] = p1;
-                    if (lane == 0) sm.keep()[warp] = keep;
+                    const float keep = exp2f(m[j] - ref), p0 = exp2f(s0 - ref), p1 = exp2f(s1 - ref);
+                    m[j] = top;
+                    l[j] = l[j] * keep + (p0 + p1);               // this lane's share of the row's sum
+                    sm.p[r][lane] = p0;
+                    sm.p[r][lane + 32] = p1;
+                    if (lane == 0) sm.keep()[r] = keep;
                 }
                 copies_wait<1>();
                 __syncthreads();                            // V and P are in
@@ -242,14 +258,18 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
             float* part = &sm.k[0][0];
 #pragma unroll
             for (int r = 0; r < kFew; ++r) part[(share * kFew + r) * D + col] = acc[r];
-            if (warp < rows) {
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+            for (int j = 0; j < kFew / kWarps; ++j) {
+                const int r = warp + j * kWarps;
+                if (r >= rows) break;
+                float sum = l[j];
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 if (lane == 0) {
-                    const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-                    sm.inv()[warp] = l == 0.0f ? 0.0f : 1.0f / l;
-                    if (!whole) a.part_lse[part_slot(blockIdx.x, begins) * kRows + warp] = lse2;
-                    else if (a.lse) a.lse[out_row(warp)] = lse2 * kLn2;
+                    const float lse2 = sum == 0.0f ? -INFINITY : m[j] + log2f(sum);
+                    sm.inv()[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    if (!whole) a.part_lse[part_slot(blockIdx.x, begins) * kRows + r] = lse2;
+                    else if (a.lse) a.lse[out_row(r)] = lse2 * kLn2;
                 }
             }
             __syncthreads();
@@ -262,39 +282,40 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                        : a.part_o + (part_slot(blockIdx.x, begins) * kRows + r) * D)[c] = x * sm.inv()[r];
             }
         } else {
-            float m[4], l[4], o[4][D / 16];
-            int top_key[4], low_key[4];                // keys [low, top] are seen
+            float m[kTR], l[kTR], o[kTR][D / 16];
+            int top_key[kTR], low_key[kTR];                // keys [low, top] are seen
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kTR; ++i) {
                 m[i] = -INFINITY;
                 l[i] = 0.0f;
-                top_key[i] = first_pos + (4 * ty + i) / a.group;
+                top_key[i] = first_pos + (kTR * ty + i) / a.group;
                 low_key[i] = a.window > 0 ? max(0, top_key[i] - a.window + 1) : 0;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) o[i][j] = 0.0f;
             }
-            const bool active = (4 * (ty & ~1)) < rows;   // warp-uniform: some row of this warp is a real one
+            const bool active = (kTR * (ty & ~1)) < rows;   // warp-uniform: some row of this warp is a real one
             for (int kt = kt0; kt < kt1; ++kt) {
-                const int key0 = (u.r.tile0 + kt) * kKeys;
-                copy_rows(a.v, &sm.v[0][0], D, key0);     // its last readers passed the barrier below
+                const int key0 = (u.r.tile0 + kt) * kKeys, slot = (kt - kt0) & 1;
+                copy_rows(a.v, &sm.v[0][0], D, slot);     // its last readers passed the barrier below
                 copies_commit();
+                if (kt + 1 < kt1) find_places(key0 + kKeys, slot ^ 1);
                 copies_wait<1>();
                 __syncthreads();                          // K (and Q) are in
-                float s[4][4];
+                float s[kTR][4];
                 if (active) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kTR; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
 #pragma unroll 4
                     for (int c = 0; c < D; c += 4) {
-                        float4 qv[4], kv[4];
+                        float4 qv[kTR], kv[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + i][c]);
+                        for (int i = 0; i < kTR; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.q[kTR * ty + i][c]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < kTR; ++i)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
@@ -304,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                             }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kTR; ++i) {
                         float top = m[i];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -322,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                         for (int j = 0; j < 4; ++j) {
                             s[i][j] = exp2f(s[i][j] - ref);
                             sum += s[i][j];
-                            sm.p[4 * ty + i][tx + 16 * j] = s[i][j];
+                            sm.p[kTR * ty + i][tx + 16 * j] = s[i][j];
                         }
                         l[i] = l[i] * keep + sum;         // this lane's share of the row's sum
 #pragma unroll
@@ -330,23 +351,23 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                     }
                 }
                 __syncthreads();                          // K is read
-                if (kt + 1 < kt1) copy_rows(a.k, &sm.k[0][0], D + 4, key0 + kKeys);
+                if (kt + 1 < kt1) copy_rows(a.k, &sm.k[0][0], D + 4, slot ^ 1);
                 copies_commit();
                 copies_wait<1>();
                 __syncthreads();                          // V is in, P is written
                 if (active) {
 #pragma unroll 2
                     for (int c = 0; c < kKeys; c += 4) {
-                        float4 pv[4];
+                        float4 pv[kTR];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(&sm.p[4 * ty + i][c]);
+                        for (int i = 0; i < kTR; ++i) pv[i] = *reinterpret_cast<const float4*>(&sm.p[kTR * ty + i][c]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
 #pragma unroll
                             for (int j = 0; j < D / 64; ++j) {
                                 const float4 x = *reinterpret_cast<const float4*>(&sm.v[c + e][4 * tx + 64 * j]);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
+                                for (int i = 0; i < kTR; ++i) {
                                     const float p = e == 0 ? pv[i].x : e == 1 ? pv[i].y : e == 2 ? pv[i].z : pv[i].w;
                                     o[i][4 * j] = fmaf(p, x.x, o[i][4 * j]);
                                     o[i][4 * j + 1] = fmaf(p, x.y, o[i][4 * j + 1]);
@@ -360,13 +381,13 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
             }
             if (active) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kTR; ++i) {
                     float sum = l[i];
 #pragma unroll
                     for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     const float lse2 = sum == 0.0f ? -INFINITY : m[i] + log2f(sum);
-                    const int r = 4 * ty + i;
+                    const int r = kTR * ty + i;
                     if (r >= rows) continue;
                     const long long orow = out_row(r), prow = part_slot(blockIdx.x, begins) * kRows + r;
 #pragma unroll
@@ -388,47 +409,50 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
             __threadfence();
             const Split sp = split_of(u, per);
             if (__syncthreads_or(tid == 0 && (claim_arrivals(a, sp, 0), arrive_last(a, sp, 0)))) {
-                const int lane = tid & 31, r0 = (tid >> 5) * 8, n = min(8, rows - r0);
-                RowMerge rm{0.0f, 0.0f, 0.0f};
-                if (lane < n) {
-                    rm = merge_row(a, sp, r0 + lane);
-                    if (a.lse) a.lse[out_row(r0 + lane)] = rm.lse * kLn2;
-                }
-                float4 acc[8];
-                float top[8], inv[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    top[r] = __shfl_sync(0xffffffffu, rm.top, r);
-                    inv[r] = __shfl_sync(0xffffffffu, rm.inv, r);
-                }
-                const int col = 4 * lane;
-#pragma unroll 2
-                for (int p = sp.first; p <= sp.last; ++p) {
-                    const long long base = sp.slot(p) * kRows + r0;
-                    float w[8];
-                    float4 x[8];
+                const int lane = tid & 31;
+                for (int r0 = (tid >> 5) * 8; r0 < rows; r0 += 8 * kWarps) {
+                    const int n = min(8, rows - r0);
+                    RowMerge rm{0.0f, 0.0f, 0.0f};
+                    if (lane < n) {
+                        rm = merge_row(a, sp, r0 + lane);
+                        if (a.lse) a.lse[out_row(r0 + lane)] = rm.lse * kLn2;
+                    }
+                    float4 acc[8];
+                    float top[8], inv[8];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const bool on = r < n && col < D;
-                        w[r] = on ? __ldcg(a.part_lse + base + r) : -INFINITY;
-                        x[r] = on ? __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + r) * D + col))
-                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        top[r] = __shfl_sync(0xffffffffu, rm.top, r);
+                        inv[r] = __shfl_sync(0xffffffffu, rm.inv, r);
+                    }
+                    const int col = 4 * lane;
+#pragma unroll 3
+                    for (int p = sp.first; p <= sp.last; ++p) {
+                        const long long base = sp.slot(p) * kRows + r0;
+                        float w[8];
+                        float4 x[8];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const bool on = r < n && col < D;
+                            w[r] = on ? __ldcg(a.part_lse + base + r) : -INFINITY;
+                            x[r] = on ? __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + r) * D + col))
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const float f = exp2f(w[r] - top[r]);
+                            acc[r].x = fmaf(f, x[r].x, acc[r].x);
+                            acc[r].y = fmaf(f, x[r].y, acc[r].y);
+                            acc[r].z = fmaf(f, x[r].z, acc[r].z);
+                            acc[r].w = fmaf(f, x[r].w, acc[r].w);
+                        }
                     }
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const float f = exp2f(w[r] - top[r]);
-                        acc[r].x = fmaf(f, x[r].x, acc[r].x);
-                        acc[r].y = fmaf(f, x[r].y, acc[r].y);
-                        acc[r].z = fmaf(f, x[r].z, acc[r].z);
-                        acc[r].w = fmaf(f, x[r].w, acc[r].w);
-                    }
+                    for (int r = 0; r < 8; ++r)
+                        if (r < n && col < D)
+                            *reinterpret_cast<float4*>(static_cast<float*>(a.o) + out_row(r0 + r) * D + col) =
+                                make_float4(acc[r].x * inv[r], acc[r].y * inv[r], acc[r].z * inv[r], acc[r].w * inv[r]);
                 }
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < n && col < D)
-                        *reinterpret_cast<float4*>(static_cast<float*>(a.o) + out_row(r0 + r) * D + col) =
-                            make_float4(acc[r].x * inv[r], acc[r].y * inv[r], acc[r].z * inv[r], acc[r].w * inv[r]);
             }
         }
         pos = u.begin + kt1;
