@@ -9,9 +9,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "gdn_attn.h"
+#include "gdn_f32x2.h"
 
 namespace gdn {
 namespace attn {
@@ -87,6 +89,8 @@ constexpr int kRows = 64, kKeys = 64, kThreads = 128, kFew = 8;
 constexpr int kWarps = kThreads / 32, kTR = kRows / (kThreads / 16);   // kTR: rows of a thread
 template <int D>
 struct SimtSmem {
+    // columns of q and p exchange their neighbouring fours (c ^ 4) in every other eight rows:
+    // a warp reads two rows eight apart at once, which would share their banks
     float q[kRows][D];
     // padded: float4 reads of 8 rows hit 32 banks; the padding holds two places in the
     // pages, of this tile's row and of the next one's
@@ -109,13 +113,58 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+// Row r of a split unit merged by a warp, its columns over the lanes, eight parts read at
+// once; every part has the weight 2^(its log-sum).
+template <int D>
+__device__ __forceinline__ void merge_row(const Args& a, const Split& sp, int r, float* to, float* lse) {
+    constexpr int AHEAD = 8;
+    const int lane = threadIdx.x & 31, col = 4 * lane;
+    float top = -INFINITY, sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p0 = sp.first; p0 <= sp.last; p0 += AHEAD) {
+        float w[AHEAD];
+        float4 x[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const long long row = (p0 + i <= sp.last ? sp.slot(p0 + i) : 0) * kRows + r;
+            w[i] = p0 + i <= sp.last ? __ldcg(a.part_lse + row) : -INFINITY;
+            x[i] = p0 + i <= sp.last && col < D ? __ldcg(reinterpret_cast<const float4*>(a.part_o + row * D + col))
+                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        float t = top;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) t = fmaxf(t, w[i]);
+        const float ref = t == -INFINITY ? 0.0f : t, keep = exp2f(top - ref);
+        top = t;
+        sum *= keep;
+        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const float f = exp2f(w[i] - ref);
+            sum += f;
+            acc.x = fmaf(f, x[i].x, acc.x);
+            acc.y = fmaf(f, x[i].y, acc.y);
+            acc.z = fmaf(f, x[i].z, acc.z);
+            acc.w = fmaf(f, x[i].w, acc.w);
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a NaN part makes the row NaN
+    if (col < D)
+        *reinterpret_cast<float4*>(to + col) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (lse && lane == 0) *lse = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
     extern __shared__ __align__(16) float smem_raw[];
     SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(smem_raw);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const Line ln = get_line<kThreads>(a, reinterpret_cast<long long*>(smem_raw));
-    if ((int)blockIdx.x >= ln.parts) return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((int)blockIdx.x >= ln.parts) {
+        if (a.merge_kernel && tid == 0) a.splits[blockIdx.x].last = -1;
+        return;
+    }
     const long long per = ln.per_part;
     long long pos = (long long)blockIdx.x * per;
     const long long end = min(pos + per, ln.total);
@@ -123,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
     Unit u = find_unit(a, seqs, pos);
     const float scale = a.scale * kLog2e;
     bool begins = true;
+    SplitUnit goes_on{-1, 0, 0, 0, 0, {}};
     for (;;) {
         const int kt0 = (int)(pos - u.begin);
         const int kt1 = (int)min((long long)u.r.tiles, end - u.begin);
@@ -159,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
         for (int n = 0; n < kRows * (D / 4) / kThreads; ++n) {
             const int i = tid + n * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
             const bool on = r < rows;
-            copy16(&sm.q[r][c],
+            copy16(&sm.q[r][c ^ (4 * ((r / kTR) & 1))],
                    static_cast<const float*>(a.q) +
                        (on ? (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.rs_q +
                                  (long long)(u.head * a.group + r % a.group) * D + c
@@ -282,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                        : a.part_o + (part_slot(blockIdx.x, begins) * kRows + r) * D)[c] = x * sm.inv()[r];
             }
         } else {
-            float m[kTR], l[kTR], o[kTR][D / 16];
+            float m[kTR], l[kTR];
+            Pair o[kTR][D / 32];                       // columns 4 tx + 64 j and the next, and the two behind them
             int top_key[kTR], low_key[kTR];                // keys [low, top] are seen
 #pragma unroll
             for (int i = 0; i < kTR; ++i) {
@@ -291,8 +342,9 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 top_key[i] = first_pos + (kTR * ty + i) / a.group;
                 low_key[i] = a.window > 0 ? max(0, top_key[i] - a.window + 1) : 0;
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) o[i][j] = 0.0f;
+                for (int j = 0; j < D / 32; ++j) o[i][j] = 0ull;
             }
+            const int swap = 4 * (ty & 1);
             const bool active = (kTR * (ty & ~1)) < rows;   // warp-uniform: some row of this warp is a real one
             for (int kt = kt0; kt < kt1; ++kt) {
                 const int key0 = (u.r.tile0 + kt) * kKeys, slot = (kt - kt0) & 1;
@@ -303,27 +355,31 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 __syncthreads();                          // K (and Q) are in
                 float s[kTR][4];
                 if (active) {
+                    Pair sum[kTR][4];   // of the even and the odd columns
 #pragma unroll
                     for (int i = 0; i < kTR; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
-#pragma unroll 4
+                        for (int j = 0; j < 4; ++j) sum[i][j] = 0ull;
+#pragma unroll 2
                     for (int c = 0; c < D; c += 4) {
-                        float4 qv[kTR], kv[4];
+                        ulonglong2 qv[kTR], kv[4];
 #pragma unroll
-                        for (int i = 0; i < kTR; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.q[kTR * ty + i][c]);
+                        for (int i = 0; i < kTR; ++i) qv[i] = *reinterpret_cast<const ulonglong2*>(&sm.q[kTR * ty + i][c ^ swap]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
+                        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(&sm.k[tx + 16 * j][c]);
 #pragma unroll
                         for (int i = 0; i < kTR; ++i)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-                                s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-                                s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-                                s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
-                            }
+                            for (int j = 0; j < 4; ++j)
+                                sum[i][j] = fma2(qv[i].y, kv[j].y, fma2(qv[i].x, kv[j].x, sum[i][j]));
                     }
+#pragma unroll
+                    for (int i = 0; i < kTR; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 t = unpair(sum[i][j]);
+                            s[i][j] = t.x + t.y;
+                        }
 #pragma unroll
                     for (int i = 0; i < kTR; ++i) {
                         float top = m[i];
@@ -343,11 +399,11 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                         for (int j = 0; j < 4; ++j) {
                             s[i][j] = exp2f(s[i][j] - ref);
                             sum += s[i][j];
-                            sm.p[kTR * ty + i][tx + 16 * j] = s[i][j];
+                            sm.p[kTR * ty + i][(tx + 16 * j) ^ swap] = s[i][j];
                         }
                         l[i] = l[i] * keep + sum;         // this lane's share of the row's sum
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j) o[i][j] *= keep;
+                        for (int j = 0; j < D / 32; ++j) o[i][j] = mul2(o[i][j], pair(keep, keep));
                     }
                 }
                 __syncthreads();                          // K is read
@@ -356,25 +412,28 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 copies_wait<1>();
                 __syncthreads();                          // V is in, P is written
                 if (active) {
-#pragma unroll 2
+#pragma unroll 1
                     for (int c = 0; c < kKeys; c += 4) {
                         float4 pv[kTR];
 #pragma unroll
-                        for (int i = 0; i < kTR; ++i) pv[i] = *reinterpret_cast<const float4*>(&sm.p[kTR * ty + i][c]);
+                        for (int i = 0; i < kTR; ++i) pv[i] = *reinterpret_cast<const float4*>(&sm.p[kTR * ty + i][c ^ swap]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 4; ++e) {
+                            ulonglong2 x[D / 64];
 #pragma unroll
-                            for (int j = 0; j < D / 64; ++j) {
-                                const float4 x = *reinterpret_cast<const float4*>(&sm.v[c + e][4 * tx + 64 * j]);
+                            for (int j = 0; j < D / 64; ++j)
+                                x[j] = *reinterpret_cast<const ulonglong2*>(&sm.v[c + e][4 * tx + 64 * j]);
 #pragma unroll
-                                for (int i = 0; i < kTR; ++i) {
-                                    const float p = e == 0 ? pv[i].x : e == 1 ? pv[i].y : e == 2 ? pv[i].z : pv[i].w;
-                                    o[i][4 * j] = fmaf(p, x.x, o[i][4 * j]);
-                                    o[i][4 * j + 1] = fmaf(p, x.y, o[i][4 * j + 1]);
-                                    o[i][4 * j + 2] = fmaf(p, x.z, o[i][4 * j + 2]);
-                                    o[i][4 * j + 3] = fmaf(p, x.w, o[i][4 * j + 3]);
+                            for (int i = 0; i < kTR; ++i) {
+                                const float p = e == 0 ? pv[i].x : e == 1 ? pv[i].y : e == 2 ? pv[i].z : pv[i].w;
+                                const Pair pp = pair(p, p);
+#pragma unroll
+                                for (int j = 0; j < D / 64; ++j) {
+                                    o[i][2 * j] = fma2(pp, x[j].x, o[i][2 * j]);
+                                    o[i][2 * j + 1] = fma2(pp, x[j].y, o[i][2 * j + 1]);
                                 }
                             }
+                        }
                     }
                 }
                 __syncthreads();                          // V and P are read
@@ -391,11 +450,12 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                     if (r >= rows) continue;
                     const long long orow = out_row(r), prow = part_slot(blockIdx.x, begins) * kRows + r;
 #pragma unroll
-                    for (int j = 0; j < D / 64; ++j)
+                    for (int j = 0; j < D / 64; ++j) {
+                        const float2 lo = unpair(o[i][2 * j]), hi = unpair(o[i][2 * j + 1]);
                         *reinterpret_cast<float4*>((whole ? static_cast<float*>(a.o) + orow * D : a.part_o + prow * D) +
                                                    4 * tx + 64 * j) =
-                            make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
-                                        o[i][4 * j + 3] * inv);
+                            make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv);
+                    }
                     if (tx == 0) {
                         if (!whole) a.part_lse[prow] = lse2;
                         else if (a.lse) a.lse[orow] = lse2 * kLn2;
@@ -404,55 +464,16 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
             }
         }
         if (!whole) {
-            // the block that brings the unit's last part merges it: eight rows a warp, a row's
-            // columns over its lanes, a few parts of all eight rows read at once
-            __threadfence();
             const Split sp = split_of(u, per);
-            if (__syncthreads_or(tid == 0 && (claim_arrivals(a, sp, 0), arrive_last(a, sp, 0)))) {
-                const int lane = tid & 31;
-                for (int r0 = (tid >> 5) * 8; r0 < rows; r0 += 8 * kWarps) {
-                    const int n = min(8, rows - r0);
-                    RowMerge rm{0.0f, 0.0f, 0.0f};
-                    if (lane < n) {
-                        rm = merge_row(a, sp, r0 + lane);
-                        if (a.lse) a.lse[out_row(r0 + lane)] = rm.lse * kLn2;
-                    }
-                    float4 acc[8];
-                    float top[8], inv[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        top[r] = __shfl_sync(0xffffffffu, rm.top, r);
-                        inv[r] = __shfl_sync(0xffffffffu, rm.inv, r);
-                    }
-                    const int col = 4 * lane;
-#pragma unroll 3
-                    for (int p = sp.first; p <= sp.last; ++p) {
-                        const long long base = sp.slot(p) * kRows + r0;
-                        float w[8];
-                        float4 x[8];
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            const bool on = r < n && col < D;
-                            w[r] = on ? __ldcg(a.part_lse + base + r) : -INFINITY;
-                            x[r] = on ? __ldcg(reinterpret_cast<const float4*>(a.part_o + (base + r) * D + col))
-                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            const float f = exp2f(w[r] - top[r]);
-                            acc[r].x = fmaf(f, x[r].x, acc[r].x);
-                            acc[r].y = fmaf(f, x[r].y, acc[r].y);
-                            acc[r].z = fmaf(f, x[r].z, acc[r].z);
-                            acc[r].w = fmaf(f, x[r].w, acc[r].w);
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        if (r < n && col < D)
-                            *reinterpret_cast<float4*>(static_cast<float*>(a.o) + out_row(r0 + r) * D + col) =
-                                make_float4(acc[r].x * inv[r], acc[r].y * inv[r], acc[r].z * inv[r], acc[r].w * inv[r]);
-                }
+            if (rows <= kFew) {
+                // the block that brings the unit's last part merges it
+                __threadfence();
+                if (__syncthreads_or(tid == 0 && (claim_arrivals(a, sp, 0), arrive_last(a, sp, 0))))
+                    for (int r = tid >> 5; r < rows; r += kWarps)
+                        merge_row<D>(a, sp, r, static_cast<float*>(a.o) + out_row(r) * D,
+                                     a.lse ? a.lse + out_row(r) : nullptr);
+            } else if (sp.first == (int)blockIdx.x && sp.last > sp.first) {
+                goes_on = SplitUnit{sp.last, sp.from_start, u.s.row0 + u.r.tok0, u.r.toks, u.head, {}};
             }
         }
         pos = u.begin + kt1;
@@ -460,6 +481,20 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
         if (pos >= end) break;
         next_unit(a, seqs, u);
     }
+    if (a.merge_kernel && tid == 0) a.splits[blockIdx.x] = goes_on;
+}
+
+// The units of many rows that the cuts split: block (i, y) the one that CTA i of the
+// attention kernel began, a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const Args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const SplitUnit u = a.splits[blockIdx.x];
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (u.last < 0 || r >= u.toks * a.group) return;
+    const long long row = (long long)(u.row0 + r / a.group) * a.num_heads + u.head * a.group + r % a.group;
+    merge_row<D>(a, Split{(int)blockIdx.x, u.last, u.from_start != 0}, r, static_cast<float*>(a.o) + row * D,
+                 a.lse ? a.lse + row : nullptr);
 }
 
 template <int D>
@@ -469,13 +504,15 @@ cudaError_t launch_simt_typed(const Args& a, cudaStream_t stream) {
         ensure_smem_limit(reinterpret_cast<const void*>(simt_kernel<D>), (int)sizeof(SimtSmem<D>), smem_set);
     if (e != cudaSuccess) return e;
     simt_kernel<D><<<a.shape.max_parts, kThreads, sizeof(SimtSmem<D>), stream>>>(a);
-    return cudaGetLastError();
+    const cudaError_t launched = cudaGetLastError();
+    if (launched != cudaSuccess || !a.merge_kernel) return launched;
+    return launch_merge(merge_kernel<D>, dim3((unsigned)a.shape.max_parts - 1, kRows / 8), a, stream);
 }
 
 }  // namespace
 
 // two CTAs per SM of a B200
-constexpr Shape kSimtShape{kRows, 1, kKeys, 296, kThreads, 2};
+constexpr Shape kSimtShape{kRows, 1, kKeys, 296, kThreads, 1, kFew};
 
 cudaError_t launch_simt(const Args& a, cudaStream_t stream) {
     return a.dim == 64 ? launch_simt_typed<64>(a, stream) : launch_simt_typed<128>(a, stream);
@@ -486,17 +523,20 @@ cudaError_t launch_simt(const Args& a, cudaStream_t stream) {
 attn::Shape paged_attention_shape(int dtype, int) { return dtype == GDN_F32 ? attn::kSimtShape : attn::shape_tc(); }
 
 attn::Layout paged_attention_layout(int dtype, int dim, int batch) {
+    constexpr size_t kMostParts = 296;   // of either kernel
     const attn::Shape sh = paged_attention_shape(dtype, dim);
     const size_t rows = (size_t)2 * sh.max_parts * sh.subs * sh.sub_rows;
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+    // What lasts from call to call (the arrival counts, back at zero after each) has its place
+    // whatever the sizes; the sequences, whose number varies, come last.
     attn::Layout l;
     l.line = sizeof(WorkspaceHeader);
-    l.seqs = l.line + sizeof(attn::Line);
-    l.arrivals = l.seqs + up(sizeof(attn::Seq) * (size_t)batch);
-    l.splits = l.arrivals + up(sizeof(unsigned long long) * (size_t)sh.max_parts * attn::kArrivals);
-    l.part_lse = l.splits + up(sizeof(attn::SplitUnit) * (size_t)sh.max_parts);
+    l.arrivals = l.line + sizeof(attn::Line);
+    l.splits = l.arrivals + up(sizeof(unsigned long long) * kMostParts * attn::kArrivals);
+    l.part_lse = l.splits + up(sizeof(attn::SplitUnit) * kMostParts);
     l.part_o = l.part_lse + up(sizeof(float) * rows);
-    l.bytes = l.part_o + up(sizeof(float) * rows * dim);
+    l.seqs = l.part_o + up(sizeof(float) * rows * dim);
+    l.bytes = l.seqs + up(sizeof(attn::Seq) * (size_t)batch);
     return l;
 }
 
@@ -507,7 +547,9 @@ cudaError_t launch_paged_attention(const attn::Args& args, cudaStream_t stream) 
     const long long step = (long long)a.block_tokens * a.shape.subs;
     a.line_inline = a.batch <= a.shape.threads && (a.rows + step - 1) / step <= 32;
     if (a.line_inline && a.batch <= 32 && a.dtype == GDN_BF16) a.line_inline = 2;   // no block barrier before the first loads
-    a.merge_kernel = a.shape.subs > 1 && a.rows > a.block_tokens;
+    // two row tiles in a unit, or more rows than its last part's CTA merges
+    a.merge_kernel = a.shape.subs > 1 ? a.rows > a.block_tokens
+                                      : std::min(a.rows, step) * a.group > a.shape.few_rows;
     if (!a.line_inline) {
         attn::line_kernel<<<1, 1024, 0, stream>>>(a);
         const cudaError_t e = cudaGetLastError();

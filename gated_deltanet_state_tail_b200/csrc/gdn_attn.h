@@ -10,8 +10,9 @@
 // GPU.  A CTA that holds a unit whole writes its outputs.  A unit that the cuts split
 // leaves normalised partial outputs and log-sums; whoever brings the last part of some
 // rows merges all of them, in the order of the line, so the result does not depend on
-// which CTA that was.  Units of two row tiles (bf16) are merged by a kernel of their own,
-// over all SMs: their parts, up to 128 KB each, took the last CTA 12 to 15 us.
+// which CTA that was.  Units of many rows (bf16: two row tiles; fp32: more than 8 rows) are
+// merged by a kernel of their own, over all SMs: their parts, up to 128 KB each, took the
+// last CTA 12 to 15 us.
 //
 // The lengths are read on the device (a captured call may be replayed with new ones).
 // When the sequences and their token blocks are few, every CTA lays out the line for
@@ -48,8 +49,7 @@ struct Line {
 };
 static_assert(sizeof(Line) == 256, "Line is 256 bytes");
 
-// A unit of two row tiles that begins in CTA i and ends in a later one, for the merging
-// kernel: slot i of a table that every CTA writes.
+// A unit of many rows that begins in CTA i and ends in a later one, for the merging kernel: slot i of a table that every CTA writes.
 struct SplitUnit {
     int last;            // its last part; -1 = there is no such unit
     int from_start;      // it begins where CTA i's stretch does
@@ -66,6 +66,7 @@ struct Shape {
     int max_parts;       // CTAs of the grid
     int threads;         // of a CTA
     int min_tiles;       // least tiles of a CTA, so that splitting pays
+    int few_rows;        // rows of a unit that its last part's CTA merges (one row tile per unit only)
 };
 
 struct Args {
@@ -92,7 +93,7 @@ struct Args {
     Line* line;
     Seq* seqs;                              // [batch]
     unsigned long long* arrivals;           // [max_parts * kArrivals]: parts of split units that are in
-    int merge_kernel;                       // there may be units of two row tiles
+    int merge_kernel;                       // there may be units that the merging kernel merges
     SplitUnit* splits;                      // [max_parts]
     float* part_lse;                        // [2 * max_parts][subs * sub_rows], base 2
     float* part_o;                          // [2 * max_parts] slots of subs * sub_rows * dim values
@@ -254,7 +255,10 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int b, bool& good) {
 __device__ __forceinline__ Line make_line(const Args& a, long long total) {
     Line ln;
     ln.total = total;
-    ln.per_part = max((total + a.shape.max_parts - 1) / a.shape.max_parts, (long long)a.shape.min_tiles);
+    // at least min_tiles a CTA, unless the line is so short that CTAs would stay idle for it
+    // (bf16, single tokens: one per CTA 10.3 and two 14.3 us for 2 tiles, 18.4 and 16.4 for 128)
+    ln.per_part = max((total + a.shape.max_parts - 1) / a.shape.max_parts,
+                      (long long)(total > 64 ? a.shape.min_tiles : 1));
     ln.parts = (int)((total + ln.per_part - 1) / ln.per_part);
     return ln;
 }
@@ -346,15 +350,20 @@ __device__ __forceinline__ Split split_of(const Unit& u, long long per) {
     return s;
 }
 
-// The arrival counts of split units sit in words tagged with the call's number, so that they
-// need no reset before the call.  claim_arrivals: each CTA of a split unit, before its part
+// The arrival counts of split units sit in words tagged for the call, so that they need no
+// reset before it.  The tag spreads the call's number over 32 bits (an odd factor, so no two
+// calls share one): what happens to be in fresh memory is small numbers more often than not.  claim_arrivals: each CTA of a split unit, before its part
 // is counted, gives the word of `share` this call's tag (and the count zero) unless another
 // has; long before the part is done, so that counting it in is a single atomic.
+__device__ __forceinline__ unsigned long long arrival_tag(const Args& a) {
+    return (unsigned long long)(a.epoch * 0x9E3779B1u ^ 0x5BD1E995u) << 32;
+}
 __device__ __forceinline__ void claim_arrivals(const Args& a, const Split& sp, int share) {
     unsigned long long* w = a.arrivals + (long long)sp.first * kArrivals + share;
     unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w);
-    while ((unsigned int)(old >> 32) != a.epoch) {   // a retry finds another part's tag: one at most
-        const unsigned long long seen = atomicCAS(w, old, (unsigned long long)a.epoch << 32);
+    const unsigned long long tag = arrival_tag(a);
+    while (old >> 32 != tag >> 32) {   // a retry finds another part's tag: one at most
+        const unsigned long long seen = atomicCAS(w, old, tag);
         if (seen == old) break;
         old = seen;
     }
@@ -366,36 +375,25 @@ __device__ __forceinline__ bool arrive_last(const Args& a, const Split& sp, int 
     unsigned long long* w = a.arrivals + (long long)sp.first * kArrivals + share;
     const unsigned int before = (unsigned int)atomicAdd(w, 1ull);
     if (before != (unsigned int)(sp.last - sp.first)) return false;
-    *reinterpret_cast<volatile unsigned long long*>(w) = (unsigned long long)a.epoch << 32;
+    *reinterpret_cast<volatile unsigned long long*>(w) = arrival_tag(a);
     __threadfence();
     return true;
 }
 
-// A split unit's row merged: every part has the weight exp2(lse - top) inv.
-struct RowMerge {
-    float top, inv, lse;   // base 2
-};
-__device__ __forceinline__ RowMerge merge_row(const Args& a, const Split& sp, int lse_row) {
-    constexpr int AHEAD = 16;   // parts read at once: the latency of a read is most of the cost
-    const int unit_rows = a.shape.subs * a.shape.sub_rows;
-    float top = -INFINITY, sum = 0.0f;
-    for (int p0 = sp.first; p0 <= sp.last; p0 += AHEAD) {
-        float x[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            x[i] = p0 + i <= sp.last ? __ldcg(a.part_lse + sp.slot(p0 + i) * unit_rows + lse_row) : -INFINITY;
-        float t = top;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) t = fmaxf(t, x[i]);
-        const float ref = t == -INFINITY ? 0.0f : t;
-        sum *= exp2f(top - ref);
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) sum += exp2f(x[i] - ref);
-        top = t;
-    }
-    const bool none = sum == 0.0f;   // a NaN part makes the sum, and so the row, NaN
-    const float ref = top == -INFINITY ? 0.0f : top;
-    return RowMerge{ref, none ? 0.0f : 1.0f / sum, none ? -INFINITY : ref + log2f(sum)};
+// Launches a merging kernel so that its blocks start as the attention kernel's leave
+// (programmatic dependent launch); they wait for all of it before they read.
+template <typename Kernel>
+inline cudaError_t launch_merge(Kernel kernel, dim3 grid, const Args& a, cudaStream_t stream) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_tc(const Args& a, cudaStream_t stream);   // bf16

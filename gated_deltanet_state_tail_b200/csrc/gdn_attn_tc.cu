@@ -34,6 +34,7 @@
 #include <cmath>
 
 #include "gdn_attn.h"
+#include "gdn_f32x2.h"
 #include "gdn_sm100.h"
 
 namespace gdn {
@@ -83,7 +84,7 @@ struct Piece {
 };
 
 struct Bars {
-    uint64_t q_full, q_free, x_full, x_free, drain[2];
+    uint64_t q_full[2], q_free[2], x_full, x_free, drain[2];
     uint64_t s_full[4], p_ready[4], o_step[4];   // per stream and buffer: 2 s + buffer
     uint64_t piece_full[2], piece_free[2];
     uint64_t kv_full[10], kv_free[10];
@@ -131,30 +132,6 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-// Two fp32 values in one 64-bit register: sm_100 adds and multiplies such pairs in one
-// instruction.
-typedef unsigned long long Pair;
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-    return p;
-}
-__device__ __forceinline__ float2 unpair(Pair p) {
-    float2 x;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(p));
-    return x;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair p;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
-    return p;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-    Pair p;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
-    return p;
 }
 
 // The largest of three, NaN if one is: a NaN score makes its row NaN whichever way its
@@ -317,6 +294,20 @@ struct Pieces {
     }
 };
 
+// Which of the two Q tiles a piece has, and how often each was used before: a piece of two
+// row tiles has both, single ones take turns, so that the next one's Q is loaded ahead.  The
+// loader and the MMA threads count alike.
+struct QTiles {
+    unsigned uses[2] = {0, 0};
+    int turn = 0;
+    __device__ __forceinline__ bool has(const Piece& p, int t) const { return !p.single || t == turn; }
+    __device__ __forceinline__ void next(const Piece& p) {
+        if (has(p, 0)) ++uses[0];
+        if (has(p, 1)) ++uses[1];
+        if (p.single) turn ^= 1;
+    }
+};
+
 // ------------------------------------------------------------------- loader
 template <int D>
 __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8_t* smem, Bars* b, int granule) {
@@ -324,23 +315,25 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
     const int lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
     const int runs = kKeys / granule;           // TMA boxes of one 64-column block
-    unsigned ring = 0, units = 0, raws = 0, raw_any = 0;   // raws: parities of v_raw
+    unsigned ring = 0, raws = 0, raw_any = 0;   // raws: parities of v_raw
+    QTiles qt;
     bool ok = true;
     Pieces pieces;
     for (Piece u = pieces.get(b); u.n > 0; u = pieces.get(b)) {
-        // Q, once the last piece's scores are done with it
-        ok = units == 0 || wait(b, &b->q_free, (units - 1) & 1);
-        if (!ok) break;
-        const int subs = u.single ? 1 : 2;
-        if (lane == 0)
-            mbar_arrive_expect_tx(&b->q_full, (uint32_t)(subs * D * 2 * a.group * a.block_tokens));
-        __syncwarp();
-        if (lane < subs * (D / 64)) {
-            const int sub = lane / (D / 64), cb = lane % (D / 64);
-            tma_load_3d(smem + S::Q + sub * S::TILE + cb * kBlock, &maps.q, &b->q_full, cb * 64, u.head * a.group,
-                        u.row0 + sub * a.block_tokens);
+        // Q, once the scores of the last piece that had the tile are done with it
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (!qt.has(u, t)) continue;
+            ok = ok && (qt.uses[t] == 0 || wait(b, &b->q_free[t], (qt.uses[t] - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&b->q_full[t], (uint32_t)(D * 2 * a.group * a.block_tokens));
+            __syncwarp();
+            if (lane < D / 64)
+                tma_load_3d(smem + S::Q + t * S::TILE + lane * kBlock, &maps.q, &b->q_full[t], lane * 64, u.head * a.group,
+                            u.row0 + (u.single ? 0 : t * a.block_tokens));
         }
-        ++units;
+        if (!ok) break;
+        qt.next(u);
         // this lane's run of rows of a tile and its page number, read a tile ahead: past the
         // pool (read as zeros) when the run holds no key of the unit
         const int run = lane % runs;
@@ -390,7 +383,8 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
         for (unsigned i = ring - n; i < ring; ++i) mbar_wait_bounded(&b->kv_full[i % S::STAGES], (i / S::STAGES) & 1, kWaitNs);
         for (int i = 0; i < S::STAGES; ++i)
             if ((raw_any >> i) & 1) mbar_wait_bounded(&b->v_raw[i], ((raws >> i) & 1) ^ 1, kWaitNs);
-        if (units) mbar_wait_bounded(&b->q_full, (units - 1) & 1, kWaitNs);
+        for (int t = 0; t < 2; ++t)
+            if (qt.uses[t]) mbar_wait_bounded(&b->q_full[t], (qt.uses[t] - 1) & 1, kWaitNs);
     }
 }
 
@@ -403,14 +397,16 @@ __device__ __forceinline__ void mma_role(const Args& a, uint8_t* smem, Bars* b, 
     using S = Smem<D>;
     const uint32_t base = smem_u32(smem), tm = b->tmem;
     const uint32_t id_s = idesc_bf16(128, kStep, false, false), id_o = idesc_bf16(128, D, false, true);
-    unsigned tiles = 0, units = 0, steps = 0, cleaned = 0;   // before this piece; parities of v_clean
+    unsigned tiles = 0, steps = 0, cleaned = 0;   // before this piece; parities of v_clean
+    QTiles qt;
     bool ok = true;
     Pieces pieces;
     for (Piece u = pieces.get_one(b); u.n > 0; u = pieces.get_one(b)) {
         // steps: single: step h is tile h, half s; else tile h / 2, half h % 2
         const bool single = u.single;
         const int H = single ? u.n : 2 * u.n;
-        const uint64_t dq = smem_desc_sw128(base + S::Q + (single ? 0 : s) * S::TILE, 16, 1024);
+        const int q = single ? qt.turn : s;   // this stream's Q tile
+        const uint64_t dq = smem_desc_sw128(base + S::Q + q * S::TILE, 16, 1024);
         // S of step h into its buffer, over the P of step h - 2, whose product has to be
         // complete: products into different accumulators are not ordered by their issue
         auto scores = [&](int h) {
@@ -429,10 +425,12 @@ __device__ __forceinline__ void mma_role(const Args& a, uint8_t* smem, Bars* b, 
             }
             mma_commit(&b->s_full[2 * s + buf]);
             if (single || half == 1) mma_commit(&b->kv_free[st]);
-            if (h == H - 1) mma_commit(&b->q_free);
+            if (h == H - 1) {   // two arrivals a tile: each stream is done with every tile of the piece
+                if (qt.has(u, 0)) mma_commit(&b->q_free[0]);
+                if (qt.has(u, 1)) mma_commit(&b->q_free[1]);
+            }
         };
-        ok = wait_one(b, &b->q_full, units & 1);
-        ++units;
+        ok = wait_one(b, &b->q_full[q], (q ? qt.uses[1] : qt.uses[0]) & 1);
         if (ok) scores(0);
         for (int h = 0; ok && h < H; ++h) {
             if (h + 1 < H) scores(h + 1);
@@ -461,6 +459,7 @@ __device__ __forceinline__ void mma_role(const Args& a, uint8_t* smem, Bars* b, 
         if (!ok) break;
         tiles += u.n;
         steps += H;
+        qt.next(u);
     }
     // everything issued is complete before the TMEM goes back
     mma_commit(&b->drain[s]);
@@ -758,11 +757,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (threadIdx.x == 0) {
-        mbar_init(&b->q_full, 1);
-        mbar_init(&b->q_free, 2);
         mbar_init(&b->x_full, 8);
         mbar_init(&b->x_free, 8);
         for (int s = 0; s < 2; ++s) {
+            mbar_init(&b->q_full[s], 1);
+            mbar_init(&b->q_free[s], 2);
             mbar_init(&b->piece_full[s], 1);
             mbar_init(&b->piece_free[s], 11);   // the softmax and MMA warps, the loader
             mbar_init(&b->drain[s], 1);
@@ -822,9 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The units of two row tiles that the cuts split, each by its parts in the order of the
 // line: block (i, share) the unit that CTA i of the attention kernel began, 32 rows of it, the
-// columns over eight warps.  23 MB of parts read once by all SMs; launched so that its blocks
-// start as the attention kernel's leave (programmatic dependent launch) and wait for the
-// rest of them.
+// columns over eight warps.  At most 23 MB of parts, read once by all SMs.
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -864,21 +861,12 @@ cudaError_t launch_typed(const Args& a, const Maps& maps, int granule, cudaStrea
     attn_tc_kernel<D><<<kMaxParts, kThreads, Smem<D>::BYTES, stream>>>(a, maps, granule);
     const cudaError_t launched = cudaGetLastError();
     if (launched != cudaSuccess || !a.merge_kernel) return launched;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(kMaxParts - 1, 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_kernel<D>, a);
+    return launch_merge(merge_kernel<D>, dim3(kMaxParts - 1, 8), a, stream);
 }
 
 }  // namespace
 
-Shape shape_tc() { return Shape{kRows, 2, kKeys, kMaxParts, kThreads, 2}; }
+Shape shape_tc() { return Shape{kRows, 2, kKeys, kMaxParts, kThreads, 2, 0}; }
 
 cudaError_t launch_tc(const Args& a, cudaStream_t stream) {
     // rows of one page that a tile's box can hold: the largest power of two that divides the

@@ -28,6 +28,7 @@
 
 #include <algorithm>
 
+#include "gdn_f32x2.h"
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -71,32 +72,6 @@ struct Vec16<__nv_bfloat16> {
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
-
-// Two fp32 values in one 64-bit register: sm_100 multiplies and adds such pairs at the
-// rate of single ones.
-struct Pair {
-    unsigned long long v;
-};
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
-    return p;
-}
-__device__ __forceinline__ float2 unpair(Pair p) {
-    float2 x;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x.x), "=f"(x.y) : "l"(p.v));
-    return x;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair p;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return p;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair p;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
-    return p;
-}
 
 enum HeadKind { kNone = -1, kQ, kK, kV };
 
