@@ -3,7 +3,7 @@
 state from the last R tokens of the matched prefix, then prefill the suffix.
 
     python bench.py [--gpus N --steps K --warmup W] [--impl ours|reference]
-                    [--workload stack|sweep|varlen|decode|outputs|overlap|fused]
+                    [--workload stack|sweep|varlen|decode|outputs|overlap|fused|hybrid]
 
 One JSON line on stdout (rank 0).  Default workload: the 24-layer stack, 32
 heads, d = 128, bf16, matched prefix L = 32768, replay R = 3277 (10%), suffix
@@ -1070,6 +1070,75 @@ def bench_overlap(args):
              "dtype": "bf16", "data": "synthetic"}]
 
 
+def bench_hybrid(args):
+    """The full-attention layers of the stack at the same cache hit (3:1, so 8 beside 24 GDN
+    layers; as wide as those: 32 heads x 128, no head sharing, bf16): the 1024-token suffix
+    behind the 32K prefix through norm + rotation + append and paged attention, then one
+    decoded token.  Each layer has its own paged cache of 64-token pages in shuffled order
+    (0.55 GB, so no layer finds its keys in L2)."""
+    import gated_deltanet_state_tail_b200 as gdn
+    wl = inputs.stack_workload(args.layers)
+    layers, H, d, page = wl.layers // GDN_PER_GROUP, wl.H, wl.dk, 64
+    L, N = wl.match_len[0], wl.suffix_len[0]
+    pages = -(-(L + N + 1) // page)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    kc = torch.empty((layers, pages, page, H, d), **bf).normal_(generator=g)
+    vc = torch.empty((layers, pages, page, H, d), **bf).normal_(generator=g)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    inv = 10000.0 ** (-torch.arange(0, d, 2, device="cuda", dtype=torch.float64) / d)
+    qw, kw = (1 + 0.2 * torch.randn(d, generator=g, device="cuda") for _ in range(2))
+    attn = gdn.PagedAttention(H, H, d, "bf16", max_batch=1, max_rows=N)
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def part(first, rows):
+        """(prepare, attend) of `rows` tokens at position `first` through every layer."""
+        qkv = torch.randn((layers, rows, 3 * H, d), generator=g, device="cuda").bfloat16()
+        pos = torch.arange(first, first + rows, device="cuda")
+        slots = table[0, pos // page].long() * page + pos % page
+        q, o = torch.empty((layers, rows, H, d), **bf), torch.empty((layers, rows, H, d), **bf)
+        cu, ctx = torch.tensor([0, rows], **i32), torch.tensor([first + rows], **i32)
+
+        def prepare():
+            for n in range(layers):
+                x = qkv[n]
+                gdn.qk_norm_rope(x[:, :H], x[:, H:2 * H], pos, inv, qw, kw, v=x[:, 2 * H:], k_cache=kc[n], v_cache=vc[n],
+                                 slots=slots, q_out=q[n])
+
+        def attend():
+            for n in range(layers):
+                attn.run(q[n], kc[n], vc[n], table, cu, ctx, o[n])
+
+        prepare()
+        attend()
+        attn.check()
+        return prepare, attend
+
+    peaks = measured_peaks()
+    flush = torch.empty(L2_FLUSH_BYTES // 4, dtype=torch.float32, device="cuda")
+    out = {"metric": f"full-attention layers of the cache hit ({layers} layers)", "unit": "ms", "higher_is_better": False,
+           "workload": f"hybrid{layers}-H{H}-d{d}-bf16-L{L}-N{N}", "layers": layers, "heads": H, "page": page,
+           "l2": "flushed before every timed part", "dtype": "bf16", "data": "synthetic"}
+    reps = max(3, min(args.steps, 20))
+    for name, first, rows in (("suffix", L, N), ("decode", L + N, 1)):
+        prepare, attend = part(first, rows)
+        prep_ms, attn_ms = _time_ms(prepare, reps, flush), _time_ms(attend, reps, flush)
+        row_bytes = rows * H * d * 2
+        pairs = rows * first + rows * (rows + 1) // 2
+        out[name] = {"norm_rope_ms": prep_ms, "attention_ms": attn_ms,
+                     "norm_rope_roofline": _hbm_roofline(layers * (6 * row_bytes + 16 * rows), prep_ms, peaks)}
+        if name == "suffix":
+            tf = 4.0 * pairs * H * d * layers / (attn_ms / 1e3) / 1e12
+            out[name]["attention_roofline"] = {"bound": "tensor", "achieved": tf, "peak": peaks["bf16_tflops"],
+                                               "unit": "TFLOP/s", "frac": tf / peaks["bf16_tflops"],
+                                               "peak_source": peaks["source"]}
+        else:
+            nbytes = layers * (2 * (first + rows) * H * d * 2 + 2 * row_bytes)
+            out[name]["attention_roofline"] = _hbm_roofline(nbytes, attn_ms, peaks)
+    out["value"] = out["suffix"]["norm_rope_ms"] + out["suffix"]["attention_ms"]
+    return [out]
+
+
 def bench_fused(args):
     """Fused replay + suffix calls against separate replay and prefill launches, on the
     24-layer cache hit (3 calls of 8 layers; 256 units and 3277-token windows, so each fused
@@ -1156,7 +1225,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--impl", choices=["ours", "reference"], default="ours")
     ap.add_argument("--workload", default="stack",
-                    choices=["stack", "sweep", "varlen", "decode", "outputs", "overlap", "fused"],
+                    choices=["stack", "sweep", "varlen", "decode", "outputs", "overlap", "fused", "hybrid"],
                     help="stack = the bench line; the others print auxiliary lines")
     ap.add_argument("--layers", type=int, default=24,
                     help="GDN layers in the stack (a multiple of 3; 24 is the bench line, "
@@ -1181,7 +1250,7 @@ def main():
 
     rank, world, local = dist_init(args.gpus)
     aux = {"sweep": bench_sweep, "varlen": bench_varlen, "decode": bench_decode, "outputs": bench_outputs,
-           "overlap": bench_overlap, "fused": bench_fused}
+           "overlap": bench_overlap, "fused": bench_fused, "hybrid": bench_hybrid}
     if args.workload in aux:
         if rank == 0:
             for line in aux[args.workload](args):

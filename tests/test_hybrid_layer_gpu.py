@@ -62,3 +62,43 @@ def test_prefix_suffix_and_decode(dtype):
         want, bound = ref.norm_rope(raw[b][:, heads:heads + kv], pos, inv, kw, 1e-6, False)
         assert bool(((ref.gather(kc, table[b], t).double() - want).abs() <= bound).all())
         assert torch.equal(ref.gather(vc, table[b], t), raw[b][:, heads + kv:])
+
+
+def test_bench_hybrid_workload():
+    """The bench's own run of the full-attention layers, one layer of them."""
+    import types
+
+    import bench
+    line, = bench.bench_hybrid(types.SimpleNamespace(layers=3, steps=3, warmup=3))
+    assert line["layers"] == 1 and line["value"] > 0
+    for part in ("suffix", "decode"):
+        assert 0 < line[part]["attention_roofline"]["frac"] < 1.5 and 0 < line[part]["norm_rope_ms"] < line["value"]
+
+
+def test_beside_gdn_layers_on_another_stream():
+    """A GDN prefill on one stream and paged attention on another give what each gives alone."""
+    from gated_deltanet_state_tail_b200 import inputs
+    t = inputs.draw_tensors(4096, 16, 128, 128, "bf16", 0.9, 0.999, 1, device="cuda")
+    plan = gdn.PrefillPlan(16, 128, 128, "bf16", [0, 1024, 2048, 3000, 4096])
+    o_gdn, st = torch.empty_like(t["v"]), torch.empty((4, 16, 128, 128), device="cuda")
+    ctx, new = [5000, 700], [300, 1]
+    cache = ref.Paged(ctx, 2, 128, 64, torch.bfloat16, 4)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randn((301, 8, 128), generator=g, device="cuda").bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = (cache.k, cache.v, cache.table, torch.tensor([0, 300, 301], **i32), torch.tensor(ctx, **i32))
+    attn = gdn.PagedAttention(8, 2, 128, "bf16", max_batch=2)
+    o = torch.empty_like(q)
+    attn.run(q, *args, o)
+    plan.run(t["q"], t["k"], t["v"], t["alpha"], t["beta"], o_gdn, state_out=st)
+    torch.cuda.synchronize()
+    want, want_gdn, want_st = o.clone(), o_gdn.clone(), st.clone()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        plan.run(t["q"], t["k"], t["v"], t["alpha"], t["beta"], o_gdn, state_out=st, stream=a)
+        attn.run(q, *args, o, stream=b)
+    torch.cuda.synchronize()
+    assert attn.status() == gdn.GDN_OK and plan.status() == gdn.GDN_OK
+    assert torch.equal(o, want) and torch.equal(o_gdn, want_gdn) and torch.equal(st, want_st)
+    plan.close()

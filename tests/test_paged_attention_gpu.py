@@ -167,13 +167,14 @@ def test_long_and_many(dtype, new, ctx):
     _case(dtype, 8, 2, 128, 64, new, ctx, seed=len(ctx))
 
 
-def test_more_sequences_than_one_scan_block():
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_sequences_than_one_scan_block(dtype):
     """The schedule's scan over the sequences takes several rounds."""
     batch = 2500
     new = [i % 3 for i in range(batch)]
     ctx = [(7 * i) % 60 + 2 for i in range(batch)]
-    cache = ref.Paged(ctx, 1, 64, 8, BF16, 31)
-    q, cu = _queries(new, 2, 64, BF16, 31), _cu(new)
+    cache = ref.Paged(ctx, 1, 64, 8, dtype, 31)
+    q, cu = _queries(new, 2, 64, dtype, 31), _cu(new)
     o, lse = _run(q, cache, cu, ctx)
     _check(q, cache, cu, ctx, o, lse)
 
@@ -301,3 +302,74 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for a, o in zip(attns, outs):
         assert a.status() == gdn.GDN_OK and torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_captured_chunks_follow_new_lengths(dtype):
+    """As above with chunks of many rows: units that the schedule splits over CTAs at one length and not at another."""
+    new, ctx = [200, 70], [2600, 70]
+    cache = ref.Paged(ctx, 2, 128, 32, dtype, 72, width=90)
+    q, cu = _queries(new, 8, 128, dtype, 72), _cu(new)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu_t, ctx_t = torch.tensor(cu, **i32), torch.tensor(ctx, **i32)
+    o, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    attn = gdn.PagedAttention(8, 2, 128, dtype, max_batch=2)
+    attn.run(q, cache.k, cache.v, cache.table, cu_t, ctx_t, o, lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn.run(q, cache.k, cache.v, cache.table, cu_t, ctx_t, o, lse)
+    for lens in ([2600, 70], [200, 70], [1031, 70], [2600, 70]):
+        ctx_t.copy_(torch.tensor(lens, **i32))
+        for _ in range(2):
+            o.fill_(SENTINEL)
+            graph.replay()
+        torch.cuda.synchronize()
+        eager, eager_lse = _run(q, cache, cu, lens, extra=0)
+        assert torch.equal(o, eager) and torch.equal(lse, eager_lse)
+        _check(q, cache, cu, lens, o, lse)
+
+
+def test_one_workspace_for_calls_of_other_sizes():
+    """Batches, head dims and dtypes in turn through one workspace of arbitrary bytes, small numbers among them."""
+    size = max(gdn.gdn_paged_attention_workspace_bytes(t, d, 400) for t in ("bf16", "f32") for d in (64, 128))
+    workspace = torch.arange(size // 4, dtype=torch.int32, device="cuda") % 512
+    cases = [(BF16, 128, [1, 1, 1], [3000, 90, 2049]), (F32, 64, [20] * 5, [700] * 5), (BF16, 64, [150] * 9, [900] * 9),
+             (BF16, 128, [1] * 400, [130] * 400), (F32, 128, [1, 2], [1500, 4000]), (BF16, 128, [300], [5000])]
+    for turn in range(3):
+        for n, (dtype, d, new, ctx) in enumerate(cases):
+            cache = ref.Paged(ctx, 2, d, 16, dtype, 90 + n)
+            q, cu = _queries(new, 8, d, dtype, 90 + n), _cu(new)
+            i32 = dict(dtype=torch.int32, device="cuda")
+            args = (torch.tensor(cu, **i32), torch.tensor(ctx, **i32))
+            o, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+            gdn.gdn_paged_attention(q, cache.k, cache.v, cache.table, *args, o, lse, workspace)
+            assert gdn.gdn_workspace_status(workspace) == gdn.GDN_OK
+            if turn == 0:
+                _check(q, cache, cu, ctx, o, lse)
+            want, want_lse = _run(q, cache, cu, ctx, extra=0)
+            assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_bad_queries_and_keys_stay_in_their_rows(dtype, bad):
+    """A NaN or infinity in one query changes no other row; one in a key changes no row that does not see it."""
+    new, ctx = [70, 1, 40], [300, 500, 40]
+    cache = ref.Paged(ctx, 2, 128, 16, dtype, 95)
+    q, cu = _queries(new, 4, 128, dtype, 95), _cu(new)
+    good, good_lse = _run(q, cache, cu, ctx)
+    x = q.clone()
+    x[33, 1, 7] = bad
+    o, lse = _run(x, cache, cu, ctx)
+    changed = (o != good).any(-1) | (lse != good_lse)
+    assert not bool(torch.isfinite(o[33, 1]).all())
+    changed[33, 1] = False
+    assert not bool(changed.any())
+    # key 20 of the third request (rows 71 .. 110 are its positions 0 .. 39), head 1 of two
+    page, row = int(cache.table[2, 20 // 16]), 20 % 16
+    cache.k[page, row, 1, 3] = bad
+    o, lse = _run(q, cache, cu, ctx)
+    same = (o == good).all(-1) & (lse == good_lse)
+    assert bool(same[:71 + 20].all()) and bool(same[:, :2].all())
+    if math.isnan(bad):
+        assert bool(torch.isnan(o[71 + 20:, 2:]).all())
