@@ -219,6 +219,20 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
         __syncthreads();   // the places are in
         copy_rows(a.k, &sm.k[0][0], D + 4, 0);
         copies_commit();
+        // Tiles with keys that some row does not see: P is 0 there, but 0 times an infinity or a
+        // NaN is not.  If such a tile of V holds one, each row skips the keys that it does not
+        // see (a thread looks through its share of the tile; the block agrees).
+        const int all_lo = a.window > 0 ? max(0, first_pos + u.r.toks - a.window) : 0;
+        auto careful = [&](int key0) {
+            if (u.r.toks == 1 || (key0 + kKeys - 1 <= first_pos && key0 >= all_lo)) return false;   // uniform
+            float acc = 0.0f;
+#pragma unroll 4
+            for (int i = tid; i < kKeys * D / 4; i += kThreads) {
+                const float4 x = reinterpret_cast<const float4*>(&sm.v[0][0])[i];
+                acc = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, fmaf(x.w, 0.0f, acc))));
+            }
+            return __syncthreads_or(acc != 0.0f) != 0;   // zero or NaN
+        };
         const bool whole = kt0 == 0 && kt1 == u.r.tiles;
         auto out_row = [&](int r) {
             return (long long)(u.s.row0 + u.r.tok0 + r / a.group) * a.num_heads + u.head * a.group + r % a.group;
@@ -288,9 +302,23 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 }
                 copies_wait<1>();
                 __syncthreads();                            // V and P are in
+                const bool skip = careful(key0);
 #pragma unroll
                 for (int r = 0; r < kFew; ++r)
                     if (r < rows) acc[r] *= sm.keep()[r];
+                if (skip) {
+#pragma unroll 1
+                    for (int n = 0; n < kKeys / SHARES; ++n) {
+                        const int k = share * (kKeys / SHARES) + (n ^ 3);   // in the order of the sums below
+                        const float x = sm.v[k][col];
+#pragma unroll
+                        for (int r = 0; r < kFew; ++r) {
+                            const int top_key = first_pos + r / a.group;
+                            if (r < rows && key0 + k <= top_key && (a.window == 0 || key0 + k > top_key - a.window))
+                                acc[r] = fmaf(sm.p[r][k], x, acc[r]);
+                        }
+                    }
+                } else
 #pragma unroll 2
                 for (int key = share * (kKeys / SHARES); key < (share + 1) * (kKeys / SHARES); key += 4) {
                     const float v0 = sm.v[key][col], v1 = sm.v[key + 1][col], v2 = sm.v[key + 2][col],
@@ -411,7 +439,26 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 copies_commit();
                 copies_wait<1>();
                 __syncthreads();                          // V is in, P is written
-                if (active) {
+                const bool skip = careful(key0);
+                if (active && skip) {
+#pragma unroll 1
+                    for (int c = 0; c < kKeys; ++c) {
+                        ulonglong2 x[D / 64];
+#pragma unroll
+                        for (int j = 0; j < D / 64; ++j)
+                            x[j] = *reinterpret_cast<const ulonglong2*>(&sm.v[c][4 * tx + 64 * j]);
+#pragma unroll
+                        for (int i = 0; i < kTR; ++i) {
+                            if (key0 + c > top_key[i] || key0 + c < low_key[i]) continue;
+                            const float p = sm.p[kTR * ty + i][c ^ swap];
+#pragma unroll
+                            for (int j = 0; j < D / 64; ++j) {
+                                o[i][2 * j] = fma2(pair(p, p), x[j].x, o[i][2 * j]);
+                                o[i][2 * j + 1] = fma2(pair(p, p), x[j].y, o[i][2 * j + 1]);
+                            }
+                        }
+                    }
+                } else if (active) {
 #pragma unroll 1
                     for (int c = 0; c < kKeys; c += 4) {
                         float4 pv[kTR];

@@ -62,7 +62,7 @@ struct Smem {
     static constexpr int KV = 2 * TILE;
     static constexpr int EXCH = KV + STAGES * TILE;           // the streams' maxima and sums: float [2][2][128]
     static constexpr int BARS = EXCH + 2048;
-    static constexpr int SCAN = BARS + 640;                   // the line's scan: a word per warp
+    static constexpr int SCAN = BARS + 704;                   // the line's scan: a word per warp
     static constexpr int BYTES = SCAN + 8 * (kThreads / 32);
 };
 
@@ -73,6 +73,7 @@ struct Piece {
     int row0, toks;        // first row of the unit's tokens in q and o, and their number
     int first_pos;         // position of the first one
     int lo, hi;            // keys that some row sees
+    int all_lo;            // the first key that the last row sees
     int key0;              // first key of the first tile
     int single;            // one row tile: the streams share it
     int slot;              // where partial results go; -1 = the unit is whole here
@@ -80,7 +81,12 @@ struct Piece {
     // the rows [from, to) of tile j that are keys of the unit
     __device__ __forceinline__ int from(int j) const { return max(0, lo - (key0 + j * kKeys)); }
     __device__ __forceinline__ int to(int j) const { return min(kKeys, hi - (key0 + j * kKeys)); }
-    __device__ __forceinline__ bool ragged(int j) const { return from(j) > 0 || to(j) < kKeys; }
+    // tile j has a key that some row does not see: beyond the first row's position or before
+    // the last row's window (which begins at `all_lo`).  Such V tiles go by the walker.
+    __device__ __forceinline__ bool tended(int j) const {
+        const int k = key0 + j * kKeys;
+        return k + kKeys - 1 > first_pos || k < all_lo;
+    }
 };
 
 struct Bars {
@@ -88,13 +94,14 @@ struct Bars {
     uint64_t s_full[4], p_ready[4], o_step[4];   // per stream and buffer: 2 s + buffer
     uint64_t piece_full[2], piece_free[2];
     uint64_t kv_full[10], kv_free[10];
-    uint64_t v_raw[10], v_clean[10];   // V tiles with rows outside the unit's keys: loaded, then zeroed there
+    uint64_t v_raw[10], v_clean[10];   // tended V tiles: loaded; fit for use
     Piece piece[2];
+    int2 dirty[4];         // per piece (counted modulo 4): first and last tile with values replaced, or (.., -1)
     uint32_t tmem;
     int abort;             // a wait ran out
     int bad_page;
 };
-static_assert(sizeof(Bars) <= 640, "the barriers fit their space");
+static_assert(sizeof(Bars) <= 704, "the barriers fit their space");
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -202,10 +209,45 @@ __device__ __forceinline__ void loaded32(float* x) {
                    "+f"(x[30]), "+f"(x[31]));
 }
 
+// Whether a V tile holds an infinity or a NaN, by a warp: any such value times zero is NaN.
+template <int D>
+__device__ __forceinline__ bool not_finite(uint32_t tile) {
+    uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 8
+    for (int i = threadIdx.x & 31; i < D * 256 / 16; i += 32) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(tile + i * 16)
+                     : "memory");
+#pragma unroll
+        for (int k = 0; k < 4; ++k) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[k]) : "r"(w[k]), "r"(0));
+    }
+    // every sum is zero (of either sign) or NaN
+    const uint32_t any = (acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu;
+    return __any_sync(0xffffffffu, any != 0u);
+}
+
+// Zeroes what is not finite in a V tile, by a warp.
+template <int D>
+__device__ __noinline__ void replace_not_finite(uint32_t tile) {
+    for (int i = threadIdx.x & 31; i < D * 256 / 4; i += 32) {
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(tile + i * 4) : "memory");
+        if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+        if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(tile + i * 4), "r"(w) : "memory");
+    }
+    __syncwarp();
+}
+
 // ------------------------------------------------------------------- walker
 // Walks this CTA's stretch of the line and hands out its pieces, one ahead of the one in
-// work, whose tiles with rows outside the unit's keys it tends: their V rows there become
-// zero before the MMA warps use the tile.
+// work, whose V tiles with keys that some row does not see it tends before the MMA threads
+// use them: P is 0 there, but 0 times an infinity or a NaN is not.  Rows outside the unit's
+// keys become zero.  Values that are not finite become zero too, and the rows that do see
+// them add them at the end; none has been found in a tile after one multiply-add by zero
+// per pair of values.
 template <int D, typename Seqs>
 __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const Seqs& seqs, uint8_t* smem, Bars* b) {
     using S = Smem<D>;
@@ -232,6 +274,7 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             p.first_pos = u.s.ctx - u.s.qlen + u.r.tok0;
             p.lo = u.r.lo;
             p.hi = u.r.hi;
+            p.all_lo = a.window > 0 ? max(0, p.first_pos + p.toks - a.window) : 0;
             p.key0 = (u.r.tile0 + kt0) * kKeys;
             p.single = u.r.toks <= a.block_tokens;
             p.slot = p.n == u.r.tiles ? -1 : (int)part_slot(blockIdx.x, i == 0);
@@ -239,6 +282,7 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             pos += p.n;
         }
         if (lane == 0) {
+            b->dirty[i & 3] = make_int2(0, -1);
             b->piece[i & 1] = p;
             mbar_arrive(&b->piece_full[i & 1]);
         }
@@ -249,18 +293,28 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             a.splits[blockIdx.x] = SplitUnit{goes_on ? p.split.last : -1, p.split.from_start, p.row0, p.toks, p.head, {}};
         }
         for (int j = 0; j < last.n; ++j, ++tiles) {
-            if (!last.ragged(j)) continue;
+            if (!last.tended(j)) continue;
             const int from = last.from(j), to = last.to(j);
             const unsigned st = (2 * tiles + 1) % S::STAGES;
             if (!wait(b, &b->v_raw[st], (tended >> st) & 1)) return;
             tended ^= 1u << st;
             const uint32_t tile = base + S::KV + st * S::TILE;
-            for (int r = lane; r < kKeys * (D / 64); r += 32) {
-                if (r % kKeys >= from && r % kKeys < to) continue;
-                const uint32_t row = tile + (r / kKeys) * kBlock + (r % kKeys) * 128;
+            if (from > 0 || to < kKeys) {
+                for (int r = lane; r < kKeys * (D / 64); r += 32) {
+                    if (r % kKeys >= from && r % kKeys < to) continue;
+                    const uint32_t row = tile + (r / kKeys) * kBlock + (r % kKeys) * 128;
 #pragma unroll
-                for (int c = 0; c < 128; c += 16)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + c), "r"(0) : "memory");
+                    for (int c = 0; c < 128; c += 16)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + c), "r"(0) : "memory");
+                }
+                __syncwarp();
+            }
+            if (last.toks > 1 && not_finite<D>(tile)) {
+                replace_not_finite<D>(tile);
+                if (lane == 0) {
+                    int2& d = b->dirty[(i - 1) & 3];
+                    d = make_int2(d.y < 0 ? j : d.x, j);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -359,7 +413,7 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
                 ok = ph == 0 || wait(b, &b->kv_free[st], (ph - 1) & 1);
                 if (!ok) break;
                 // a ragged V tile goes to the walker first; its own phase then passes empty
-                const bool raw = kv == 1 && u.ragged(j);
+                const bool raw = kv == 1 && u.tended(j);
                 uint64_t* full = raw ? &b->v_raw[st] : &b->kv_full[st];
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full, S::TILE);
@@ -438,7 +492,7 @@ __device__ __forceinline__ void mma_role(const Args& a, uint8_t* smem, Bars* b, 
             const unsigned G = steps + h, buf = G & 1, at = 2 * (tiles + (single ? h : h >> 1)) + 1, st = at % S::STAGES;
             const int half = single ? s : h & 1;
             if (single || half == 0) {
-                if (u.ragged(single ? h : h >> 1)) {   // the walker's word that it is clean
+                if (u.tended(single ? h : h >> 1)) {   // the walker's word that it is clean
                     ok = wait_one(b, &b->v_clean[st], (cleaned >> st) & 1);
                     cleaned ^= 1u << st;
                 } else {
@@ -651,6 +705,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         const long long orow =
             (long long)(u.row0 + sub * a.block_tokens + row_tok) * a.num_heads + u.head * a.group + row_head;
         const bool whole = u.slot < 0;
+        const int2 dirty = b->dirty[(pieces.i - 1) & 3];
         // Partial outputs of this warp's rows (single: of this group's half of their columns):
         // [columns / 4][R] float4 with R the rows of the warp, rounded up to a power of two, so
         // that both the writes (a lane per row) and the merge's reads are of whole lines.
@@ -685,6 +740,26 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = fmaf(z[i], f1, o[i]);
+                }
+                if (__builtin_expect(dirty.y >= 0, 0)) {
+                    // the values that the walker replaced, for the rows that see them
+                    const int k0 = max(max(low_key, u.lo), u.key0 + dirty.x * kKeys);
+                    const int k1 = min(min(top_key + 1, u.hi), u.key0 + (dirty.y + 1) * kKeys);
+#pragma unroll 1
+                    for (int key = k0; key < k1; ++key) {
+                        if (!u.tended((key - u.key0) / kKeys)) continue;
+                        const int page = a.page_table[(long long)u.b * a.max_pages + key / a.page_size];
+                        if (page < 0 || page >= a.num_pages) continue;
+                        const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                            static_cast<const __nv_bfloat16*>(a.v) + (long long)page * a.page_stride +
+                            (long long)(key % a.page_size) * a.row_stride + (long long)u.head * a.head_stride + c * 32);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t w = v[i];
+                            if ((w & 0x7f80u) == 0x7f80u) o[2 * i] += __uint_as_float(w << 16);
+                            if ((w & 0x7f800000u) == 0x7f800000u) o[2 * i + 1] += __uint_as_float(w & 0xffff0000u);
+                        }
+                    }
                 }
                 if (row < rows) {
                     if (whole) {

@@ -364,8 +364,8 @@ GDN_API size_t gdn_paged_attention_workspace_bytes(int32_t dtype, int32_t head_d
  * A row that sees no key (L = 0, or more rows than context) gets o = 0 and
  * lse = -infinity.  Cache rows outside the context or before every row's window
  * are not used, whatever they hold, and page numbers of pages that hold only
- * such rows are not read.  A key that some row of a sequence sees must have
- * finite values in v.
+ * such rows are not read.  Infinities and NaN in q, k and v reach only the rows
+ * that see them: padding behind a sequence's tokens may hold anything.
  *   q            [rows, num_heads, head_dim] (row stride of the descriptor)
  *   page_table   [batch, max_pages] int32: page of key j of sequence b is
  *                page_table[b][j / page_size].

@@ -373,3 +373,53 @@ def test_bad_queries_and_keys_stay_in_their_rows(dtype, bad):
     assert bool(same[:71 + 20].all()) and bool(same[:, :2].all())
     if math.isnan(bad):
         assert bool(torch.isnan(o[71 + 20:, 2:]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("d,heads,window", [(128, 4, 0), (64, 2, 0), (128, 16, 0), (64, 12, 90), (128, 2, 33)])
+def test_bad_values_reach_only_rows_that_see_them(dtype, bad, d, heads, window):
+    """A value that is not finite, in one column of one key: rows that see the key have it in that column, nothing else
+    of any row changes by a bit."""
+    new, ctx = [70, 1, 300, 6], [300, 500, 2000, 6]
+    cache = ref.Paged(ctx, 2, d, 16, dtype, 96)
+    q, cu = _queries(new, heads, d, dtype, 96), _cu(new)
+    good, good_lse = _run(q, cache, cu, ctx, window)
+    group = heads // 2
+    for b, pos in ((0, 260), (0, 299), (2, 1701), (2, 1850), (2, 1999), (3, 0), (3, 5), (1, 499), (2, 1650)):
+        at = (int(cache.table[b, pos // 16]), pos % 16, 1, 7)
+        was = cache.v[at].clone()
+        cache.v[at] = bad
+        o, lse = _run(q, cache, cu, ctx, window)
+        cache.v[at] = was
+        first = ctx[b] - new[b]
+        rows = torch.arange(cu[b], cu[b + 1], device="cuda")
+        row_pos = rows - cu[b] + first
+        sees = rows[(row_pos >= pos) & ((row_pos - pos < window) | (window == 0))]
+        want = good.clone()
+        want[sees, group:, 7] = bad
+        assert torch.equal(o.nan_to_num(nan=1e9), want.nan_to_num(nan=1e9)), (b, pos)
+        assert torch.equal(lse, good_lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_padded_chunks(dtype):
+    """A padded batch: every request has 64 rows, its real tokens first; what the padding holds reaches no real row."""
+    real, ctx_real = [64, 10, 1, 33], [500, 10, 77, 1033]
+    new = [64] * 4
+    ctx = [c - r + 64 for c, r in zip(ctx_real, real)]      # the padding's rows are in the cache too
+    cache = ref.Paged(ctx, 2, 128, 16, dtype, 97)
+    q, cu = _queries(new, 8, 128, dtype, 97), _cu(new)
+    want = {}
+    for b, (r, c) in enumerate(zip(real, ctx_real)):
+        for (r0, r1), o, bound, _, _ in ref.attention(q[cu[b]:cu[b] + r], cache.k, cache.v, cache.table[b:b + 1], [0, r], [c],
+                                                      128 ** -0.5, 0):
+            want[b] = (o, bound)
+        at = torch.arange(c, ctx[b], device="cuda")
+        rows = cache.table[b][at // 16].long(), at % 16
+        cache.k[rows], cache.v[rows] = math.nan, math.inf
+        q[cu[b] + r:cu[b + 1]] = math.nan
+    o, _ = _run(q, cache, cu, ctx)
+    for b, r in enumerate(real):
+        w, bound = want[b]
+        assert bool(((o[cu[b]:cu[b] + r].double() - w).abs() <= bound).all()), b
