@@ -209,19 +209,23 @@ __device__ __forceinline__ void loaded32(float* x) {
                    "+f"(x[30]), "+f"(x[31]));
 }
 
-// Whether a V tile holds an infinity or a NaN, by a warp: any such value times zero is NaN.
+// Whether rows [r0, r1) of a V tile hold an infinity or a NaN, by a warp: any such value
+// times zero is NaN.
 template <int D>
-__device__ __forceinline__ bool not_finite(uint32_t tile) {
+__device__ __forceinline__ bool not_finite(uint32_t tile, int r0, int r1) {
     uint32_t acc[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 8
-    for (int i = threadIdx.x & 31; i < D * 256 / 16; i += 32) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(tile + i * 16)
-                     : "memory");
 #pragma unroll
-        for (int k = 0; k < 4; ++k) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[k]) : "r"(w[k]), "r"(0));
+    for (int cb = 0; cb < D / 64; ++cb) {
+#pragma unroll 4
+        for (int i = r0 * 8 + (threadIdx.x & 31); i < r1 * 8; i += 32) {   // 8 pieces of 16 bytes a row
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(tile + cb * kBlock + i * 16)
+                         : "memory");
+#pragma unroll
+            for (int k = 0; k < 4; ++k) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[k]) : "r"(w[k]), "r"(0));
+        }
     }
     // every sum is zero (of either sign) or NaN
     const uint32_t any = (acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu;
@@ -309,7 +313,11 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
                 }
                 __syncwarp();
             }
-            if (last.toks > 1 && not_finite<D>(tile)) {
+            // the keys that some row sees and some row does not: before the last row's window,
+            // and beyond the first row's position
+            const int key0 = last.key0 + j * kKeys;
+            const int before = min(to, last.all_lo - key0), beyond = max(from, last.first_pos + 1 - key0);
+            if (last.toks > 1 && (not_finite<D>(tile, from, before) || not_finite<D>(tile, beyond, to))) {
                 replace_not_finite<D>(tile);
                 if (lane == 0) {
                     int2& d = b->dirty[(i - 1) & 3];
