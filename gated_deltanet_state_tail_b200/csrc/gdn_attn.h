@@ -3,10 +3,11 @@
 //
 // The work is cut by key tiles.  A unit is a block of consecutive new tokens of one
 // sequence with the query heads of one key head (rows = tokens x heads of the group);
-// its cost is the number of key tiles that its causal (and window) range touches.  The
-// units' tiles, in the order (sequence, key head, token block), form one line of `total`
-// tiles, and each of `parts` CTAs takes the same length of it, wherever units begin and
-// end.  So one long context with one new token and a thousand short ones both fill the
+// its length is the number of key tiles that its causal (and window) range touches, and
+// unit_extra more at its end for what a unit costs beside its tiles.  The units, in the order
+// (sequence, key head, token block), form one line of length `total`, and each of `parts`
+// CTAs takes the same length of it, wherever units begin and end (without the extra, the CTA
+// with a prompt's short first blocks took 115 us where the others took 75).  So one long context with one new token and a thousand short ones both fill the
 // GPU.  A CTA that holds a unit whole writes its outputs.  A unit that the cuts split
 // leaves normalised partial outputs and log-sums; whoever brings the last part of some
 // rows merges all of them, in the order of the line, so the result does not depend on
@@ -35,21 +36,22 @@ struct Seq {
     int qlen;            // new tokens; 0 if its descriptor entries are bad
     int ctx;             // context length, the new tokens included
     int pad;
-    long long head_tiles; // key tiles of one key head, over its token blocks
-    long long before;    // tiles of the sequences before it
+    long long head_len;  // length of one key head's units on the line
+    long long before;    // length of the sequences before it
 };
 static_assert(sizeof(Seq) == 32, "Seq is 32 bytes");
 
 // The line, in the workspace after the status header.
 struct Line {
-    long long total;     // tiles
-    long long per_part;  // tiles of each CTA (the last may have fewer)
+    long long total;
+    long long per_part;  // length of each CTA's stretch (the last may have less)
     int parts;           // CTAs with work
     int pad[59];
 };
 static_assert(sizeof(Line) == 256, "Line is 256 bytes");
 
-// A unit of many rows that begins in CTA i and ends in a later one, for the merging kernel: slot i of a table that every CTA writes.
+// A unit of many rows that begins in CTA i and ends in a later one, for the merging kernel:
+// slot i of a table that every CTA writes.
 struct SplitUnit {
     int last;            // its last part; -1 = there is no such unit
     int from_start;      // it begins where CTA i's stretch does
@@ -65,7 +67,8 @@ struct Shape {
     int tile_keys;       // keys of a tile
     int max_parts;       // CTAs of the grid
     int threads;         // of a CTA
-    int min_tiles;       // least tiles of a CTA, so that splitting pays
+    int min_tiles;       // least length of a CTA's stretch, so that splitting pays
+    int unit_extra;      // a unit's cost beside its tiles, in tiles
     int few_rows;        // rows of a unit that its last part's CTA merges (one row tile per unit only)
 };
 
@@ -134,7 +137,7 @@ struct Unit {
     int b, head, t;      // sequence, key head, token block
     Range r;
     Seq s;
-    long long begin;     // tile of the line where it begins
+    long long begin;     // where it begins on the line
 };
 
 // The sequences of the line as find_unit and next_unit see them, for a whole warp: in the
@@ -166,7 +169,7 @@ struct LaneSeqs {
         s.qlen = __shfl_sync(0xffffffffu, mine.qlen, b);
         s.ctx = __shfl_sync(0xffffffffu, mine.ctx, b);
         s.pad = 0;
-        s.head_tiles = __shfl_sync(0xffffffffu, mine.head_tiles, b);
+        s.head_len = __shfl_sync(0xffffffffu, mine.head_len, b);
         s.before = __shfl_sync(0xffffffffu, mine.before, b);
         return s;
     }
@@ -175,7 +178,7 @@ struct LaneSeqs {
     }
 };
 
-// The unit that holds tile `pos` of the line (0 <= pos < total), by a whole warp.
+// The unit that holds place `pos` of the line (0 <= pos < total), by a whole warp.
 template <typename Seqs>
 __device__ __forceinline__ Unit find_unit(const Args& a, const Seqs& seqs, long long pos) {
     const int lane = threadIdx.x & 31;
@@ -183,14 +186,14 @@ __device__ __forceinline__ Unit find_unit(const Args& a, const Seqs& seqs, long 
     u.b = seqs.find(pos);
     u.s = seqs.get(u.b);
     const long long in = pos - u.s.before;
-    u.head = ((in | u.s.head_tiles) >> 32) ? (int)(in / u.s.head_tiles)
-                                           : (int)((uint32_t)in / (uint32_t)u.s.head_tiles);
-    const long long rem = in - u.head * u.s.head_tiles;
+    u.head = ((in | u.s.head_len) >> 32) ? (int)(in / u.s.head_len)
+                                           : (int)((uint32_t)in / (uint32_t)u.s.head_len);
+    const long long rem = in - u.head * u.s.head_len;
     const int blocks = token_blocks(a, u.s.qlen);
     long long done = 0;
-    for (int t0 = 0;; t0 += 32) {                    // ends: rem < head_tiles = the sum over all blocks
+    for (int t0 = 0;; t0 += 32) {                    // ends: rem < head_len = the sum over all blocks
         const int t = t0 + lane;
-        const int n = t < blocks ? block_range(a, u.s.qlen, u.s.ctx, t).tiles : 0;
+        const int n = t < blocks ? block_range(a, u.s.qlen, u.s.ctx, t).tiles + a.shape.unit_extra : 0;
         int incl = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -201,7 +204,7 @@ __device__ __forceinline__ Unit find_unit(const Args& a, const Seqs& seqs, long 
         if (hit || t0 + 32 >= blocks) {
             const int l = hit ? __ffs(hit) - 1 : 31;
             u.t = t0 + l;
-            u.begin = u.s.before + u.head * u.s.head_tiles + done + __shfl_sync(0xffffffffu, incl - n, l);
+            u.begin = u.s.before + u.head * u.s.head_len + done + __shfl_sync(0xffffffffu, incl - n, l);
             break;
         }
         done += __shfl_sync(0xffffffffu, incl, 31);
@@ -210,10 +213,15 @@ __device__ __forceinline__ Unit find_unit(const Args& a, const Seqs& seqs, long 
     return u;
 }
 
+// Where the unit after u begins, or the line ends.
+__device__ __forceinline__ long long unit_end(const Args& a, const Unit& u) {
+    return u.begin + u.r.tiles + a.shape.unit_extra;
+}
+
 // The unit after u on the line (the caller knows that there is one).
 template <typename Seqs>
 __device__ __forceinline__ void next_unit(const Args& a, const Seqs& seqs, Unit& u) {
-    u.begin += u.r.tiles;
+    u.begin = unit_end(a, u);
     if (++u.t >= token_blocks(a, u.s.qlen)) {
         u.t = 0;
         if (++u.head >= a.num_kv_heads) {
@@ -228,7 +236,7 @@ __device__ __forceinline__ void next_unit(const Args& a, const Seqs& seqs, Unit&
     u.r = block_range(a, u.s.qlen, u.s.ctx, u.t);
 }
 
-// Checks sequence b's entries and counts its tiles, by one thread (WARP = false) or a whole
+// Checks sequence b's entries and adds up its units, by one thread (WARP = false) or a whole
 // warp.  Entries that do not fit the call's extents give no work: the rows stay as they were.
 template <bool WARP>
 __device__ __forceinline__ Seq load_seq(const Args& a, int b, bool& good) {
@@ -243,12 +251,13 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int b, bool& good) {
     s.before = 0;
     long long n = 0;
     const int blocks = token_blocks(a, s.qlen);
-    for (int t = lane; t < blocks; t += WARP ? 32 : 1) n += block_range(a, s.qlen, ctx, t).tiles;
+    for (int t = lane; t < blocks; t += WARP ? 32 : 1)
+        n += block_range(a, s.qlen, ctx, t).tiles + a.shape.unit_extra;
     if (WARP) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
     }
-    s.head_tiles = n;
+    s.head_len = n;
     return s;
 }
 
@@ -272,7 +281,7 @@ __device__ __forceinline__ Line lane_line(const Args& a, LaneSeqs& seqs) {
         bool good;
         seqs.mine = load_seq<false>(a, lane, good);
         if (!good) tag_merge_inline(&a.ws->status, a.epoch, kStatusMismatch, false);
-        n = seqs.mine.head_tiles * a.num_kv_heads;
+        n = seqs.mine.head_len * a.num_kv_heads;
     }
     long long incl = n;
 #pragma unroll
@@ -303,7 +312,7 @@ __device__ __forceinline__ Line get_line(const Args& a, long long* scratch) {
         bool good;
         s = load_seq<false>(a, b, good);
         if (!good) tag_merge_inline(&a.ws->status, a.epoch, kStatusMismatch, false);
-        n = s.head_tiles * a.num_kv_heads;
+        n = s.head_len * a.num_kv_heads;
     }
     long long incl = n;
 #pragma unroll
@@ -327,8 +336,8 @@ __device__ __forceinline__ Line get_line(const Args& a, long long* scratch) {
     return make_line(a, total);
 }
 
-// Where a CTA leaves its part of a split unit: two slots per CTA, one for the unit that its
-// stretch of the line begins with and one for the unit that it ends with.
+// Where a CTA leaves its part of a split unit: two slots per CTA, one for the unit that has
+// begun by the start of its stretch of the line and one for a unit that begins after it.
 __device__ __forceinline__ long long part_slot(long long part, bool begins_stretch) {
     return 2 * part + (begins_stretch ? 0 : 1);
 }
@@ -352,9 +361,10 @@ __device__ __forceinline__ Split split_of(const Unit& u, long long per) {
 
 // The arrival counts of split units sit in words tagged for the call, so that they need no
 // reset before it.  The tag spreads the call's number over 32 bits (an odd factor, so no two
-// calls share one): what happens to be in fresh memory is small numbers more often than not.  claim_arrivals: each CTA of a split unit, before its part
-// is counted, gives the word of `share` this call's tag (and the count zero) unless another
-// has; long before the part is done, so that counting it in is a single atomic.
+// calls share one): what happens to be in fresh memory is small numbers more often than not.
+// claim_arrivals: each CTA of a split unit, before its part is counted, gives the word of
+// `share` this call's tag (and the count zero) unless another has; long before the part is
+// done, so that counting it in is a single atomic.
 __device__ __forceinline__ unsigned long long arrival_tag(const Args& a) {
     return (unsigned long long)(a.epoch * 0x9E3779B1u ^ 0x5BD1E995u) << 32;
 }

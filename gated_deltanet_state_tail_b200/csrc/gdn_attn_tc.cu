@@ -1,7 +1,7 @@
 // gdn_attn_tc.cu -- bf16 attention of new tokens over a paged cache on the tensor cores
 // (tcgen05 + TMA); the formulas are in gdn_attn.cu, the division of the work in gdn_attn.h.
 //
-// One persistent CTA per SM walks its stretch of the line of key tiles (128 keys).  Ten
+// One persistent CTA per SM walks its stretch of the line of key tiles (128 keys).  Twelve
 // warps work: a loader, two MMA issuers, a walker along the line and two groups of four
 // softmax warps.
 //   - A row tile holds 128 / group tokens, each with the query heads of one key head, so
@@ -258,18 +258,24 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
     const int lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
     const long long per = ln.per_part;
-    long long pos = (long long)blockIdx.x * per;
-    const long long end = min(pos + per, ln.total);
+    const long long start = (long long)blockIdx.x * per, end = min(start + per, ln.total);
     Unit u{};
-    if (pos < end) u = find_unit(a, seqs, pos);
+    bool more = start < end;   // u has tiles in the stretch
+    if (more) {
+        u = find_unit(a, seqs, start);
+        if (start - u.begin >= u.r.tiles) {
+            more = unit_end(a, u) < end;
+            if (more) next_unit(a, seqs, u);
+        }
+    }
     unsigned tiles = 0, tended = 0;   // before the piece being tended; parities of v_raw
     Piece last;
     last.n = 0;
     for (unsigned i = 0;; ++i) {
         if (i >= 2 && !wait(b, &b->piece_free[i & 1], (i / 2 - 1) & 1)) return;
         Piece p{};
-        if (pos < end) {
-            const int kt0 = (int)(pos - u.begin), kt1 = (int)min((long long)u.r.tiles, end - u.begin);
+        if (more) {
+            const int kt0 = (int)max(0ll, start - u.begin), kt1 = (int)min((long long)u.r.tiles, end - u.begin);
             p.n = kt1 - kt0;
             p.b = u.b;
             p.head = u.head;
@@ -281,9 +287,9 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             p.all_lo = a.window > 0 ? max(0, p.first_pos + p.toks - a.window) : 0;
             p.key0 = (u.r.tile0 + kt0) * kKeys;
             p.single = u.r.toks <= a.block_tokens;
-            p.slot = p.n == u.r.tiles ? -1 : (int)part_slot(blockIdx.x, i == 0);
+            p.slot = p.n == u.r.tiles ? -1 : (int)part_slot(blockIdx.x, u.begin <= start);
             p.split = split_of(u, per);
-            pos += p.n;
+            more = unit_end(a, u) < end;
         }
         if (lane == 0) {
             b->dirty[i & 3] = make_int2(0, -1);
@@ -291,7 +297,7 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             mbar_arrive(&b->piece_full[i & 1]);
         }
         __syncwarp();
-        if (a.merge_kernel && lane == 0 && pos >= end && (p.n > 0 || i == 0)) {   // the stretch's last piece
+        if (a.merge_kernel && lane == 0 && !more && (p.n > 0 || i == 0)) {   // the stretch's last piece
             const bool goes_on = p.n > 0 && !p.single && p.slot >= 0 && p.split.first == (int)blockIdx.x &&
                                  p.split.last > p.split.first;
             a.splits[blockIdx.x] = SplitUnit{goes_on ? p.split.last : -1, p.split.from_start, p.row0, p.toks, p.head, {}};
@@ -330,7 +336,7 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
         }
         last = p;
         if (p.n == 0) return;
-        if (pos < end) next_unit(a, seqs, u);
+        if (more) next_unit(a, seqs, u);
     }
 }
 
@@ -603,6 +609,19 @@ struct Merge {
 };
 
 // ------------------------------------------------------------ softmax groups
+// The lanes whose bit BIT of the lane number is 0 give their y and the others their x to the
+// lane across.
+template <int BIT>
+__device__ __forceinline__ void trade(uint32_t (&x)[4], uint32_t (&y)[4]) {
+    const bool upper = threadIdx.x & BIT;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[i] : y[i], BIT);
+        if (upper) x[i] = got;
+        else y[i] = got;
+    }
+}
+
 template <int D>
 __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars* b, int s) {
     using S = Smem<D>;
@@ -769,20 +788,29 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                         }
                     }
                 }
-                if (row < rows) {
-                    if (whole) {
-                        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + c * 32);
+                if (whole) {
+                    // four lanes trade their rows' 16-byte pieces, so that they store 64 bytes of
+                    // one row at a time (a lane per row: 32 lines a store, 4 us a unit)
+                    uint32_t w[4][4];   // [piece of my row], then [row of the four][word of piece lane % 4]
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            to[i] = make_uint4(pack(o[8 * i], o[8 * i + 1]), pack(o[8 * i + 2], o[8 * i + 3]),
-                                               pack(o[8 * i + 4], o[8 * i + 5]), pack(o[8 * i + 6], o[8 * i + 7]));
-                    } else {
-                        float4* to = reinterpret_cast<float4*>(a.part_o + (long long)u.slot * (2 * kRows * D) + warp_at) +
-                                     (c - c0) * 8 * R + lane;
+                    for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = pack(o[2 * i], o[2 * i + 1]);
+                    trade<1>(w[0], w[1]);
+                    trade<1>(w[2], w[3]);
+                    trade<2>(w[0], w[2]);
+                    trade<2>(w[1], w[3]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            to[i * R] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const long long to = __shfl_sync(0xffffffffu, orow, (lane & ~3) + i);
+                        if (quarter * 32 + (lane & ~3) + i < rows)
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + to * D + c * 32 + (lane & 3) * 8) =
+                                make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
                     }
+                } else if (row < rows) {
+                    float4* to = reinterpret_cast<float4*>(a.part_o + (long long)u.slot * (2 * kRows * D) + warp_at) +
+                                 (c - c0) * 8 * R + lane;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        to[i * R] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             }
             if (row < rows) {
@@ -949,7 +977,9 @@ cudaError_t launch_typed(const Args& a, const Maps& maps, int granule, cudaStrea
 
 }  // namespace
 
-Shape shape_tc() { return Shape{kRows, 2, kKeys, kMaxParts, kThreads, 2, 0}; }
+// unit_extra 2 (a unit's start and output, beside tiles of about 2 us): a prompt of 4096 tokens
+// and 32 chunks of new tokens took 127 and 34 us with 0, 93 and 31 with 2, 93 and 35 with 6.
+Shape shape_tc() { return Shape{kRows, 2, kKeys, kMaxParts, kThreads, 2, 2, 0}; }
 
 cudaError_t launch_tc(const Args& a, cudaStream_t stream) {
     // rows of one page that a tile's box can hold: the largest power of two that divides the
