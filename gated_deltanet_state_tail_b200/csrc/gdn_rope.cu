@@ -73,10 +73,11 @@ struct Vec16<__nv_bfloat16> {
     }
 };
 
-enum HeadKind { kNone = -1, kQ, kK, kV };
-
 // Block: RT consecutive rows (blockIdx.x) and the heads of one of gridDim.y shares; the
-// lane groups are dealt to the rows, and each walks its row's share of the q, k and v heads.
+// lane groups are dealt to the rows, and each walks its row's share of the q heads, then of
+// the k heads, then of the v heads, each with a loop of its own: with one loop that asked
+// for every head which of them it was, a head cost 180 instructions a warp instead of 85
+// and issue slots bounded the 67001-row case (174 us).
 template <typename T, int D, int RT, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeArgs a) {
     using V = Vec16<T>;
@@ -84,41 +85,43 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeAr
     constexpr int LPH = D / N;                  // lanes of one head
     constexpr int GROUPS = kThreads / LPH;      // heads in flight in the block
     static_assert(GROUPS % RT == 0, "every row gets the same number of lane groups");
+    static_assert(RT == 1 || RT >= 32 / LPH, "the lane groups of a warp walk the same heads, of different rows");
     constexpr int GPR = GROUPS / RT;            // lane groups of one row
     __shared__ float2 cs[RT][D / 2];
 
     const long long row_base = (long long)blockIdx.x * RT;
-    const int group = threadIdx.x / LPH, l = threadIdx.x % LPH;
+    const int group = threadIdx.x / LPH, l = threadIdx.x % LPH, lane = threadIdx.x & 31;
+    const unsigned lanes = RT > 1 || LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1) << (lane - l);   // that walk as this one
     const int rl = group % RT;
     const long long row = row_base + rl;
     const bool row_ok = row < a.rows;
     const int e0 = l * N;                       // first element of this lane
 
-    // this lane's heads, hh = first_head + it * step: q heads, then k heads, then (with a
-    // cache) v heads; the number of rounds is the same for every lane: shuffles stay whole
+    // this lane's heads: every step-th of q, k and (with a cache) v heads in a row, so that few
+    // rows spread their heads evenly
     const int Hq = a.num_heads, Hkv = a.num_kv_heads;
-    const int heads = Hq + (a.slots ? 2 : 1) * Hkv;
     const int step = GPR * gridDim.y;
-    const int first_head = group / RT + GPR * blockIdx.y;
-    const int rounds = (heads + step - 1) / step;
-    auto kind_of = [&](int hh) { return hh < Hq ? kQ : hh < Hq + Hkv ? kK : hh < heads ? kV : kNone; };
+    auto first_from = [&](int h, int count) {   // in the list after one of `count` heads entered at h
+        return h >= count ? h - count : h + (count - h + step - 1) / step * step - count;
+    };
+    const int hq = group / RT + GPR * blockIdx.y;
+    const int hk = first_from(hq, Hq);
+    const int hv = first_from(hk, Hkv);
     const T* q = static_cast<const T*>(a.q) + row * a.rs_q + e0;
     const T* k = static_cast<const T*>(a.k) + row * a.rs_k + e0;
     const T* v = static_cast<const T*>(a.v) + row * a.rs_v + e0;
     uint4 raw[kAhead];
-    auto load = [&](int it0) {
+    auto load = [&](const T* list, int h, int count) {
+        const T* from = list + (long long)h * D;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int hh = first_head + (it0 + i) * step;
-            const HeadKind kind = row_ok ? kind_of(hh) : kNone;
             raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (kind != kNone)
-                raw[i] = *reinterpret_cast<const uint4*>(kind == kQ   ? q + (long long)hh * D
-                                                         : kind == kK ? k + (long long)(hh - Hq) * D
-                                                                      : v + (long long)(hh - Hq - Hkv) * D);
+            if (row_ok && h + i * step < count) raw[i] = *reinterpret_cast<const uint4*>(from);
+            from += (long long)step * D;
         }
     };
-    load(0);
+    if (hq < Hq) load(q, hq, Hq);
+    else if (hk < Hkv) load(k, hk, Hkv);
     T* k_page = nullptr;
     T* v_page = nullptr;
     if (row_ok && a.slots) {
@@ -151,100 +154,96 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeAr
     const bool rot = e0 < a.rotary_dim;
     // the lane of the pair's other half (split halves); half is a multiple of N
     const bool upper = e0 >= half;
-    const int lane = threadIdx.x & 31;
     const int partner = !rot ? lane : lane - l + (upper ? l - half / N : l + half / N);
     const int pe0 = INTERLEAVED || !rot ? e0 : upper ? e0 - half : e0 + half;   // its first element
 
-    Pair A[N / 2], B[N / 2];
+    // norm and rotation of this lane's heads of one list; `store` gets each with its number
+    auto walk = [&](const T* list, int h, int count, const float* w, bool loaded, auto store) {
+        if (h >= count) return;
+        Pair A[N / 2], B[N / 2];
+        float wo[N], wp[N], av[N], bv[N];
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) A[i] = B[i] = pair(0.0f, 0.0f);
-    HeadKind have = kNone;       // whose constants A and B are
-    bool normed = false;
-    for (int it0 = 0; it0 < rounds; it0 += kAhead) {
-        if (it0) load(it0);
+        for (int i = 0; i < N; ++i) wo[i] = wp[i] = 1.0f;
+        if (w) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (it0 + u >= rounds) break;
-            const int hh = first_head + (it0 + u) * step;
-            const HeadKind kind = row_ok ? kind_of(hh) : kNone;
-            if (kind == kV && v_page)              // the values go in as they came
-                *reinterpret_cast<uint4*>(v_page + (hh - Hq - Hkv) * a.cache_head_stride) = raw[u];
-            const bool turn = kind == kQ || kind == kK;
-            if (!__any_sync(0xffffffffu, turn)) continue;
-            if (turn && kind != have) {
-                have = kind;
-                const float* w = kind == kQ ? a.q_weight : a.k_weight;
-                normed = w != nullptr;
-                float wo[N], wp[N], av[N], bv[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) wo[i] = wp[i] = 1.0f;
-                if (normed) {
-#pragma unroll
-                    for (int i = 0; i < N; i += 4) {
-                        *reinterpret_cast<float4*>(wo + i) = *reinterpret_cast<const float4*>(w + e0 + i);
-                        *reinterpret_cast<float4*>(wp + i) = *reinterpret_cast<const float4*>(w + pe0 + i);
-                    }
-                }
-                const int c0 = INTERLEAVED ? e0 / 2 : upper ? e0 - half : e0;   // this lane's first angle
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float2 x = rot ? cs[rl][INTERLEAVED ? c0 + i / 2 : c0 + i] : make_float2(1.0f, 0.0f);
-                    const bool first = INTERLEAVED ? i % 2 == 0 : !upper;   // a pair's first element: minus
-                    av[i] = wo[i] * x.x;
-                    bv[i] = wp[INTERLEAVED ? i ^ 1 : i] * (first ? -x.y : x.y);
-                }
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    A[i] = pair(av[2 * i], av[2 * i + 1]);
-                    B[i] = pair(bv[2 * i], bv[2 * i + 1]);
-                }
-            }
-            float xs[N];
-            V::unpack(raw[u], xs);
-            Pair x[N / 2], sq = pair(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                x[i] = pair(xs[2 * i], xs[2 * i + 1]);
-                sq = fma2(x[i], x[i], sq);
-            }
-            const float2 sums = unpair(sq);
-            float ss = sums.x + sums.y;
-#pragma unroll
-            for (int m = LPH / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            const float r = normed ? rsqrtf(ss * (1.0f / D) + a.eps) : 1.0f;
-            float os[N];
-            if constexpr (INTERLEAVED) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) os[i] = xs[i ^ 1];
-            } else {
-                uint4 other;
-                other.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
-                other.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
-                other.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
-                other.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
-                V::unpack(other, os);
-            }
-            if (!turn) continue;
-            // x A before r: an x whose square is finite is far from overflowing there
-            const Pair rr = pair(r, r);
-            float z[N];
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                Pair t = mul2(x[i], A[i]);
-                if (rot) t = fma2(pair(os[2 * i], os[2 * i + 1]), B[i], t);
-                const float2 y = unpair(mul2(t, rr));
-                z[2 * i] = y.x;
-                z[2 * i + 1] = y.y;
-            }
-            const uint4 out = V::pack(z);
-            if (kind == kQ) {
-                *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + (row * Hq + hh) * D + e0) = out;
-            } else {
-                const int h = hh - Hq;
-                if (a.k_out) *reinterpret_cast<uint4*>(static_cast<T*>(a.k_out) + (row * Hkv + h) * D + e0) = out;
-                if (k_page) *reinterpret_cast<uint4*>(k_page + h * a.cache_head_stride) = out;
+            for (int i = 0; i < N; i += 4) {
+                *reinterpret_cast<float4*>(wo + i) = *reinterpret_cast<const float4*>(w + e0 + i);
+                *reinterpret_cast<float4*>(wp + i) = *reinterpret_cast<const float4*>(w + pe0 + i);
             }
         }
+        const int c0 = INTERLEAVED ? e0 / 2 : upper ? e0 - half : e0;   // this lane's first angle
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 x = rot ? cs[rl][INTERLEAVED ? c0 + i / 2 : c0 + i] : make_float2(1.0f, 0.0f);
+            const bool first = INTERLEAVED ? i % 2 == 0 : !upper;   // a pair's first element: minus
+            av[i] = wo[i] * x.x;
+            bv[i] = wp[INTERLEAVED ? i ^ 1 : i] * (first ? -x.y : x.y);
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            A[i] = pair(av[2 * i], av[2 * i + 1]);
+            B[i] = pair(bv[2 * i], bv[2 * i + 1]);
+        }
+        for (; h < count; h += kAhead * step, loaded = false) {
+            if (!loaded) load(list, h, count);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int head = h + u * step;
+                if (head >= count) break;
+                float xs[N];
+                V::unpack(raw[u], xs);
+                Pair x[N / 2], sq = pair(0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    x[i] = pair(xs[2 * i], xs[2 * i + 1]);
+                    sq = fma2(x[i], x[i], sq);
+                }
+                const float2 sums = unpair(sq);
+                float ss = sums.x + sums.y;
+#pragma unroll
+                for (int m = LPH / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(lanes, ss, m);
+                const float r = w ? rsqrtf(ss * (1.0f / D) + a.eps) : 1.0f;
+                float os[N];
+                if constexpr (INTERLEAVED) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) os[i] = xs[i ^ 1];
+                } else {
+                    uint4 other;
+                    other.x = __shfl_sync(lanes, raw[u].x, partner);
+                    other.y = __shfl_sync(lanes, raw[u].y, partner);
+                    other.z = __shfl_sync(lanes, raw[u].z, partner);
+                    other.w = __shfl_sync(lanes, raw[u].w, partner);
+                    V::unpack(other, os);
+                }
+                // x A before r: an x whose square is finite is far from overflowing there
+                const Pair rr = pair(r, r);
+                float z[N];
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    Pair t = mul2(x[i], A[i]);
+                    if (rot) t = fma2(pair(os[2 * i], os[2 * i + 1]), B[i], t);
+                    const float2 y = unpair(mul2(t, rr));
+                    z[2 * i] = y.x;
+                    z[2 * i + 1] = y.y;
+                }
+                if (row_ok) store(head, V::pack(z));
+            }
+        }
+    };
+    T* q_out = static_cast<T*>(a.q_out) + row * Hq * D + e0;
+    walk(q, hq, Hq, a.q_weight, true, [&](int h, uint4 out) { *reinterpret_cast<uint4*>(q_out + h * D) = out; });
+    T* k_out = a.k_out ? static_cast<T*>(a.k_out) + row * Hkv * D + e0 : nullptr;
+    walk(k, hk, Hkv, a.k_weight, hq >= Hq, [&](int h, uint4 out) {
+        if (k_out) *reinterpret_cast<uint4*>(k_out + h * D) = out;
+        if (k_page) *reinterpret_cast<uint4*>(k_page + h * a.cache_head_stride) = out;
+    });
+    if (!a.slots) return;
+    for (int h = hv; h < Hkv; h += kAhead * step) {   // the values go in as they came
+        load(v, h, Hkv);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (v_page && h + u * step < Hkv)
+                *reinterpret_cast<uint4*>(v_page + (h + u * step) * a.cache_head_stride) = raw[u];
     }
 }
 
