@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
         // Tiles with keys that some row does not see: P is 0 there, but 0 times an infinity or a
         // NaN is not.  If such a tile of V holds one, each row skips the keys that it does not
         // see (a thread looks through its share of the tile; the block agrees).
-        const int all_lo = a.window > 0 ? max(0, first_pos + u.r.toks - a.window) : 0;
+        const int all_lo = first_key(a, first_pos + u.r.toks - 1);
         auto careful = [&](int key0) {
             if (u.r.toks == 1 || (key0 + kKeys - 1 <= first_pos && key0 >= all_lo)) return false;   // uniform
             float acc = 0.0f;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                     const int r = warp + j * kWarps;
                     if (r >= rows) break;
                     const int top_key = first_pos + r / a.group;
-                    const int low_key = a.window > 0 ? max(0, top_key - a.window + 1) : 0;
+                    const int low_key = first_key(a, top_key);
                     float s0 = sm.p[r][lane], s1 = sm.p[r][lane + 32];
                     const int k0 = key0 + lane, k1 = k0 + 32;
                     s0 = k0 >= low_key && k0 <= top_key ? s0 : -INFINITY;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 m[i] = -INFINITY;
                 l[i] = 0.0f;
                 top_key[i] = first_pos + (kTR * ty + i) / a.group;
-                low_key[i] = a.window > 0 ? max(0, top_key[i] - a.window + 1) : 0;
+                low_key[i] = first_key(a, top_key[i]);
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) o[i][j] = 0ull;
             }

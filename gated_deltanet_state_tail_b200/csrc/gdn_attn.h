@@ -4,14 +4,16 @@
 // The work is cut by key tiles.  A unit is a block of consecutive new tokens of one
 // sequence with the query heads of one key head (rows = tokens x heads of the group);
 // its length is the number of key tiles that its causal (and window) range touches, and
-// unit_extra more at its end for what a unit costs beside its tiles.  The units, in the order
-// (sequence, key head, token block), form one line of length `total`, and each of `parts`
-// CTAs takes the same length of it, wherever units begin and end (without the extra, the CTA
-// with a prompt's short first blocks took 115 us where the others took 75).  So one long context with one new token and a thousand short ones both fill the
-// GPU.  A CTA that holds a unit whole writes its outputs.  A unit that the cuts split
-// leaves normalised partial outputs and log-sums; whoever brings the last part of some
-// rows merges all of them, in the order of the line, so the result does not depend on
-// which CTA that was.  Units of many rows (bf16: two row tiles; fp32: more than 8 rows) are
+// unit_extra more at its end for what a unit costs beside its tiles.  The units, in the
+// order (sequence, key head, token block), form one line of length `total`, and each of
+// `parts` CTAs takes the same length of it, wherever units begin and end.  So one long
+// context with one new token and a thousand short ones both fill the GPU.  (Without the
+// extra, the CTAs with a prompt's short first blocks took 115 us where others took 75.)
+//
+// A CTA that holds a unit whole writes its outputs.  A unit that the cuts split leaves
+// normalised partial outputs and log-sums; whoever brings the last part of some rows
+// merges all of them, in the order of the line, so the result does not depend on which
+// CTA that was.  Units of many rows (bf16: two row tiles; fp32: more than 8 rows) are
 // merged by a kernel of their own, over all SMs: their parts, up to 128 KB each, took the
 // last CTA 12 to 15 us.
 //
@@ -28,6 +30,7 @@
 namespace gdn {
 namespace attn {
 
+constexpr int kMostKeys = 1 << 30;   // of a context: sums of positions and tile sizes stay in an int
 constexpr int kArrivals = 8;     // separately merged shares of a split unit's rows, at most
 
 // One sequence of the line, 32 bytes.
@@ -113,6 +116,11 @@ struct Range {
     int tile0, tiles;    // key tiles; at least one, so that rows without keys are written too
 };
 
+// The first key that a row sees which sees none after `top` (which may be negative).
+__device__ __forceinline__ int first_key(const Args& a, int top) {
+    return a.window > 0 && top >= a.window ? top - a.window + 1 : 0;
+}
+
 __device__ __forceinline__ Range block_range(const Args& a, int qlen, int ctx, int t) {
     Range r;
     const int step = a.block_tokens * a.shape.subs;
@@ -120,8 +128,7 @@ __device__ __forceinline__ Range block_range(const Args& a, int qlen, int ctx, i
     r.toks = min(step, qlen - r.tok0);
     const int first = ctx - qlen + r.tok0;           // position of the first row (may be negative)
     r.hi = max(0, first + r.toks);
-    r.lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
-    r.lo = min(r.lo, r.hi);
+    r.lo = min(first_key(a, first), r.hi);
     r.tile0 = r.lo / a.shape.tile_keys;
     r.tiles = max(1, (r.hi + a.shape.tile_keys - 1) / a.shape.tile_keys - r.tile0);
     return r;
@@ -242,7 +249,8 @@ template <bool WARP>
 __device__ __forceinline__ Seq load_seq(const Args& a, int b, bool& good) {
     const int lane = WARP ? threadIdx.x & 31 : 0;
     const int r0 = a.cu[b], r1 = a.cu[b + 1], ctx = a.ctx[b];
-    good = r0 >= 0 && r1 >= r0 && r1 <= a.rows && ctx >= 0 && ctx <= (long long)a.max_pages * a.page_size;
+    good = r0 >= 0 && r1 >= r0 && r1 <= a.rows && ctx >= 0 && ctx <= kMostKeys &&
+           ctx <= (long long)a.max_pages * a.page_size;
     Seq s;
     s.row0 = r0;
     s.qlen = good ? r1 - r0 : 0;

@@ -51,7 +51,8 @@ constexpr int kMaxParts = 148;     // one CTA per SM of a B200
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a row's maximum that P absorbs
-constexpr int kPoly = 5;           // of 16 pairs of exponentials, those on the FMA pipe (measured: 0 .. 8)
+constexpr int kPoly = 5;           // of 16 pairs of exponentials, those on the FMA pipe; a prompt of 4096
+                                   // tokens takes 98, 97, 95, 96 and 98 us with 0, 3, 5, 6 and 8
 constexpr int kBlock = kKeys * 128;   // bytes of one 64-column block of a 128-row tile
 
 template <int D>
@@ -284,7 +285,7 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             p.first_pos = u.s.ctx - u.s.qlen + u.r.tok0;
             p.lo = u.r.lo;
             p.hi = u.r.hi;
-            p.all_lo = a.window > 0 ? max(0, p.first_pos + p.toks - a.window) : 0;
+            p.all_lo = first_key(a, p.first_pos + p.toks - 1);
             p.key0 = (u.r.tile0 + kt0) * kKeys;
             p.single = u.r.toks <= a.block_tokens;
             p.slot = p.n == u.r.tiles ? -1 : (int)part_slot(blockIdx.x, u.begin <= start);
@@ -641,10 +642,10 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         const int rows = toks * a.group;
         const int first_pos = u.first_pos + sub * a.block_tokens;
         const int top_key = row < rows ? first_pos + row_tok : -1;     // keys [low_key, top_key] are seen
-        const int low_key = a.window > 0 ? max(0, top_key - a.window + 1) : 0;
+        const int low_key = first_key(a, top_key);
         // keys that every row of the tile sees: [all_lo, all_hi]
         const int all_hi = first_pos;
-        const int all_lo = a.window > 0 ? max(0, first_pos + toks - a.window) : 0;
+        const int all_lo = first_key(a, first_pos + toks - 1);
         const bool active = quarter * 32 < rows;   // this warp has rows
         // while the first scores are on their way
         if (active && u.slot >= 0 && u.single && lane == 0) claim_arrivals(a, u.split, s * 4 + quarter);
@@ -932,7 +933,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The units of two row tiles that the cuts split, each by its parts in the order of the
 // line: block (i, share) the unit that CTA i of the attention kernel began, 32 rows of it, the
-// columns over eight warps.  At most 23 MB of parts, read once by all SMs.
+// columns over eight warps.  At most 38 MB of parts (two a CTA), read once by
+// all SMs.
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

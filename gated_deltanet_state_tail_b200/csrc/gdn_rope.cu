@@ -13,9 +13,10 @@
 // Every element is read once and written once with about 7 flops in between, so HBM
 // bounds it.  16 bytes per lane: one head is 8 to 32 lanes, the sum of squares a
 // shuffle tree over them in fp32, x' (split halves) one shuffle of the raw 16 bytes.
-// Four heads are loaded ahead, the first four before the angles are computed: with one
-// at a time the 67001-row case (824 MB) took 317 us.  The result is rounded once, from
-// fp32, when it is stored.
+// Four heads are loaded ahead, the first four before the angles are computed: the
+// 67001-row case (24 heads of 128, bf16, 824 MB) takes 146 us so, 5.7 TB/s, and took 213,
+// 170 and 172 us with one, two and eight.  The result is rounded once, from fp32, when it
+// is stored.
 //
 // The angle is exact for far positions without a table and without fp64 per pair: a
 // turn is 2^64, so p f_i mod 2 pi is the low 64 bits of p times the frequency in turns
@@ -76,8 +77,8 @@ struct Vec16<__nv_bfloat16> {
 // Block: RT consecutive rows (blockIdx.x) and the heads of one of gridDim.y shares; the
 // lane groups are dealt to the rows, and each walks its row's share of the q heads, then of
 // the k heads, then of the v heads, each with a loop of its own: with one loop that asked
-// for every head which of them it was, a head cost 180 instructions a warp instead of 85
-// and issue slots bounded the 67001-row case (174 us).
+// for every head which of them it was, a warp issued 181 instructions for its two heads
+// instead of 114 and the 67001-row case was bound by that (174 us).
 template <typename T, int D, int RT, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeArgs a) {
     using V = Vec16<T>;
@@ -263,7 +264,7 @@ cudaError_t launch_rt(const NormRopeArgs& a, cudaStream_t stream) {
 // One row per block while the rows are few, so that a row's heads spread over all lane
 // groups; eight rows per block otherwise, and one per lane group (at most 16) once that
 // still gives two blocks per SM: A and B then last for all heads of a row (67001 rows of 24
-// heads: 256, 203 and 187 us with 4, 8 and 16 rows).
+// heads: 234, 174 and 146 us with 4, 8 and 16 rows; 1024 rows of 96: 18 us with each).
 template <typename T, int D, bool IL>
 cudaError_t launch_rows(const NormRopeArgs& a, cudaStream_t stream) {
     constexpr int GROUPS = kThreads / (D / Vec16<T>::N);

@@ -371,7 +371,7 @@ GDN_API size_t gdn_paged_attention_workspace_bytes(int32_t dtype, int32_t head_d
  *                page_table[b][j / page_size].
  *   cu_seqlens   [batch + 1] int32, non-decreasing, within 0 .. rows; rows
  *                that no sequence owns are left untouched.
- *   context_len  [batch] int32, 0 .. max_pages * page_size.
+ *   context_len  [batch] int32, 0 .. max_pages * page_size, at most 2^30.
  *   o_out        [rows, num_heads, head_dim] packed, the cache's dtype; not q.
  *   lse_out      [rows, num_heads] fp32 (natural log), or NULL.
  *   workspace    gdn_paged_attention_workspace_bytes(dtype, head_dim, batch).

@@ -423,3 +423,31 @@ def test_padded_chunks(dtype):
     for b, r in enumerate(real):
         w, bound = want[b]
         assert bool(((o[cu[b]:cu[b] + r].double() - w).abs() <= bound).all()), b
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 300, 1000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_windows_beyond_every_context(dtype, window):
+    """A window that no context reaches changes nothing, for rows without keys beside rows with some too."""
+    new, ctx = [300, 1, 40], [120, 999, 700]
+    cache = ref.Paged(ctx, 2, 64, 16, dtype, 91)
+    q, cu = _queries(new, 6, 64, dtype, 91), _cu(new)
+    o, lse = _run(q, cache, cu, ctx, window)
+    _check(q, cache, cu, ctx, o, lse)
+    all_o, all_lse = _run(q, cache, cu, ctx)
+    assert torch.equal(o, all_o) and torch.equal(lse, all_lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_contexts_beyond_the_largest_are_reported(dtype):
+    cache = ref.Paged([50, 50], 1, 64, 8, dtype, 92)
+    q = _queries([1, 1], 1, 64, dtype, 92)
+    good, _ = _run(q, cache, [0, 1, 2], [50, 50])
+    table = torch.zeros((2, 2 ** 27 + 1), dtype=torch.int32, device="cuda")   # room for 2^30 + 8 keys a row
+    table[:, :cache.table.shape[1]] = cache.table
+    attn = gdn.PagedAttention(1, 1, 64, dtype, max_batch=2)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o = torch.full(q.shape, SENTINEL, dtype=dtype, device="cuda")
+    attn.run(q, cache.k, cache.v, table, torch.tensor([0, 1, 2], **i32), torch.tensor([50, 2 ** 30 + 1], **i32), o)
+    assert attn.status() == gdn.GDN_ERR_MISMATCH
+    assert torch.equal(o[:1], good[:1]) and bool((o[1:] == SENTINEL).all())
