@@ -44,6 +44,29 @@ def test_norm_and_rotation(dtype, d, rot, interleaved, rows, heads, kv):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_rows(dtype, d, interleaved):
+    """Enough rows for the widest row blocks, the last block not full, and keys and values appended."""
+    rows, heads, kv, page = 4741, 5, 3, 16
+    q, k, v, pos, inv, qw, kw = _inputs(dtype, rows, heads, kv, d, 32, 40000, 8)
+    pages = -(-rows // page)
+    kc = torch.full((pages, page, kv, d), 7.0, dtype=dtype, device="cuda")
+    vc = torch.full_like(kc, 7.0)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:rows]
+    qo, ko = gdn.qk_norm_rope(q, k, pos, inv, qw, kw, interleaved=interleaved, v=v, k_cache=kc, v_cache=vc, slots=slots,
+                              k_out=torch.empty((rows, kv, d), dtype=dtype, device="cuda"))
+    _close(qo, ref.norm_rope(q, pos, inv, qw, 1e-6, interleaved), "q")
+    _close(ko, ref.norm_rope(k, pos, inv, kw, 1e-6, interleaved), "k")
+    assert torch.equal(kc.view(-1, kv, d)[slots], ko) and torch.equal(vc.view(-1, kv, d)[slots], v)
+    rest = torch.ones(pages * page, dtype=torch.bool, device="cuda")
+    rest[slots] = False
+    assert bool((kc.view(-1, kv, d)[rest] == 7).all()) and bool((vc.view(-1, kv, d)[rest] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("far", [0, 1, 131072, 10 ** 6, 2 ** 31, 2 ** 40])
 def test_far_positions(dtype, far):
     q, k, v, pos, inv, qw, kw = _inputs(dtype, 33, 4, 2, 128, 128, far, 5)
