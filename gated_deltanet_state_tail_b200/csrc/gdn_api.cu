@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "gdn_attn.h"
+#include "gdn_hybrid.h"
 #include "gdn_internal.h"
 #include "gdn_tail_replay.h"
 

@@ -25,7 +25,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "gdn_internal.h"
+#include "gdn_hybrid.h"
 
 namespace gdn {
 namespace attn {

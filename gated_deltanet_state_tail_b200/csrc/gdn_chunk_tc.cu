@@ -44,6 +44,7 @@
 #include <cuda_runtime.h>
 
 #include "gdn_chunk_common.h"
+#include "gdn_hybrid.h"
 
 namespace gdn {
 namespace {

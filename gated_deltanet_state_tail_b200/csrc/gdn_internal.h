@@ -68,8 +68,8 @@ unsigned int next_call_number();
 // another thread's change, and a word changes at most a few times per call (one
 // retag, then once per status bit), so the loop ends; the cap only bounds it.  Out
 // of line: inlined at every wait site, the loop slowed the prefill kernel by 3%.
-__device__ __forceinline__ void tag_merge_inline(unsigned long long* word, unsigned int epoch, unsigned int val,
-                                                 bool first_only) {
+static __device__ __noinline__ void tag_merge(unsigned long long* word, unsigned int epoch, unsigned int val,
+                                          bool first_only) {
     unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
     for (int i = 0; i < 64; ++i) {
         const unsigned int low = (unsigned int)(old >> 32) == epoch ? (unsigned int)old : 0u;
@@ -80,10 +80,6 @@ __device__ __forceinline__ void tag_merge_inline(unsigned long long* word, unsig
         if (seen == old) return;
         old = seen;
     }
-}
-static __device__ __noinline__ void tag_merge(unsigned long long* word, unsigned int epoch, unsigned int val,
-                                          bool first_only) {
-    tag_merge_inline(word, epoch, val, first_only);
 }
 
 // Index checks of the debug build (compiled with -DGDN_DEBUG_BOUNDS).  Each
@@ -206,32 +202,6 @@ struct DecodeArgs {
     void* o_out;
 };
 
-// Norm, rotation and cache append of new tokens' projections (no plan, no workspace).
-struct NormRopeArgs {
-    int dtype;                   // gdn_dtype of q, k, v, the outputs and the cache
-    int num_heads, num_kv_heads;
-    int dim, rotary_dim;
-    int interleaved;             // pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)
-    long long rows;
-    long long rs_q, rs_k, rs_v;  // elements between consecutive rows
-    float eps;
-    const void* q;
-    const void* k;
-    const void* v;               // with a cache only
-    const long long* positions;  // [rows]
-    const double* inv_freq;      // [rotary_dim / 2]
-    const float* q_weight;       // [dim] or null: q is not normalised
-    const float* k_weight;
-    void* q_out;                 // [rows, num_heads, dim] packed
-    void* k_out;                 // [rows, num_kv_heads, dim] packed, or null
-    // the paged cache, or slots = null
-    const long long* slots;      // [rows]: page * page_size + row in the page; outside the pool = not written
-    void* k_pages;
-    void* v_pages;
-    int num_pages, page_size;
-    long long page_stride, cache_row_stride, cache_head_stride;   // elements
-};
-
 // Raise a kernel's dynamic shared-memory limit once per device (a kernel attribute
 // is per device); safe when several host threads launch at once.
 inline cudaError_t ensure_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& done_devices) {
@@ -259,7 +229,6 @@ inline long long row_stride_v(const gdn_varlen_desc* d) {
 
 cudaError_t launch_recurrent(const CallArgs& a, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
-cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const CallArgs& a, cudaStream_t stream);   // dispatches the replay below
 cudaError_t launch_replay_tc(const CallArgs& a, cudaStream_t stream);
 cudaError_t launch_replay_ws(const CallArgs& a, cudaStream_t stream);

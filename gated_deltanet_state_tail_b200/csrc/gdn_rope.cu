@@ -30,7 +30,7 @@
 #include <algorithm>
 
 #include "gdn_f32x2.h"
-#include "gdn_internal.h"
+#include "gdn_hybrid.h"
 
 namespace gdn {
 namespace {
