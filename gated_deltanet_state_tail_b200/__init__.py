@@ -486,8 +486,10 @@ def _qk_desc(*fields):
 
 
 @functools.lru_cache(maxsize=256)
-def _attn_desc(*fields):
-    return gdn_attn_desc(*fields)
+def _attn_desc(batch, num_heads, rows, q_row_stride, max_pages, window, scale):
+    if not 0 <= window < 2 ** 31:   # ctypes would take its low 32 bits
+        raise ValueError("window must be 0 (all keys) to 2^31 - 1")
+    return gdn_attn_desc(batch, num_heads, rows, q_row_stride, max_pages, window, scale, 0)
 
 
 def _paged_kv(k_cache, v_cache):
@@ -586,7 +588,7 @@ def gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len
     if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"the workspace must be contiguous and have at least {need} bytes")
     d = _attn_desc(batch, heads, rows, _row_stride(q_shape, q.stride(), "q"), width, int(window),
-                   dim ** -0.5 if scale is None else scale, 0)
+                   dim ** -0.5 if scale is None else scale)
     status = _fn("gdn_paged_attention")(
         ctypes.byref(d), ctypes.byref(c), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
         cu_seqlens.data_ptr(), context_len.data_ptr(), o_out.data_ptr(), lse_ptr, workspace.data_ptr(),

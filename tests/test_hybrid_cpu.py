@@ -151,3 +151,10 @@ def test_python_refuses_host_tensors_and_shapes():
     d = gdn._paged_kv(c.transpose(1, 2).contiguous().transpose(1, 2), c.transpose(1, 2).contiguous().transpose(1, 2))
     assert (d.page_stride, d.row_stride, d.head_stride) == (2 * 16 * 128, 128, 16 * 128)
     assert gdn._paged_kv(c, c.clone()).page_stride == 0
+
+
+@pytest.mark.parametrize("window", [-1, 2 ** 31, 2 ** 32 + 5])
+def test_python_refuses_windows_that_do_not_fit(window):
+    with pytest.raises(ValueError):
+        gdn._attn_desc(1, 8, 4, 0, 2, window, 1.0)
+    assert gdn._attn_desc(1, 8, 4, 0, 2, 2 ** 31 - 1, 1.0).window == 2 ** 31 - 1
