@@ -516,8 +516,10 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
         if (!whole) {
             const Split sp = split_of(u, per);
             if (rows <= kFew) {
-                // the block that brings the unit's last part merges it
+                // the block that brings the unit's last part merges it; the part counts as in once
+                // every thread has written its share
                 __threadfence();
+                __syncthreads();
                 if (__syncthreads_or(tid == 0 && (claim_arrivals(a, sp, 0), arrive_last(a, sp, 0))))
                     for (int r = tid >> 5; r < rows; r += kWarps)
                         merge_row<D>(a, sp, r, static_cast<float*>(a.o) + out_row(r) * D,

@@ -1,0 +1,69 @@
+"""Paged attention called again and again: split units, captured and concurrent calls and the device's reports, for both
+types.  Bounds: tests/hybrid_reference.py."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import gated_deltanet_state_tail_b200 as gdn
+import hybrid_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+SENTINEL = 77.0
+
+
+def _i32(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+class Call:
+    """A paged cache, queries and the arguments of one call over them."""
+
+    def __init__(self, dtype, heads, kv, d, page, new, ctx, seed, width=None):
+        self.new, self.ctx, self.dtype = new, ctx, dtype
+        self.cache = ref.Paged(ctx, kv, d, page, dtype, seed, width=width)
+        g = torch.Generator(device="cuda")
+        g.manual_seed(1000 + seed)
+        self.q = torch.randn((sum(new), heads, d), generator=g, device="cuda").to(dtype)
+        self.cu = [0] + list(itertools.accumulate(new))
+        self.cu_t, self.ctx_t = _i32(self.cu), _i32(ctx)
+
+    def attention(self):
+        return gdn.PagedAttention(self.q.shape[1], self.cache.k.shape[2], self.q.shape[2], self.dtype, max_batch=len(self.ctx))
+
+    def outputs(self):
+        return torch.full_like(self.q, SENTINEL), torch.full(self.q.shape[:2], SENTINEL, device="cuda")
+
+    def run(self, attn, o, lse=None, table=None, cu=None, ctx=None, **kw):
+        attn.run(self.q, self.cache.k, self.cache.v, self.cache.table if table is None else table,
+                 self.cu_t if cu is None else cu, self.ctx_t if ctx is None else ctx, o, lse, **kw)
+
+    def check(self, o, lse, ctx=None):
+        for (r0, r1), want, bound, want_lse, lse_bound in ref.attention(
+                self.q, self.cache.k, self.cache.v, self.cache.table, self.cu, ctx or self.ctx, self.q.shape[2] ** -0.5, 0):
+            assert bool(((o[r0:r1].double() - want).abs() <= bound).all()), (r0, r1)
+            assert bool(((lse[r0:r1].double() - want_lse).abs() <= lse_bound).all()), (r0, r1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,kv,new", [(1, 1, 1), (8, 2, 1), (8, 1, 1), (8, 8, 1), (4, 2, 3), (8, 2, 2)])
+def test_split_units_of_few_rows_over_and_over(dtype, d, heads, kv, new):
+    """1 to 8 rows over a long context, cut over many CTAs: whoever merges has all of every part, so that each of many
+    calls, from a workspace that holds NaN, gives the bits of the first."""
+    call = Call(dtype, heads, kv, d, 16, [new], [9000 + 7 * heads + new], seed=d + heads + new)
+    attn = call.attention()
+    first, first_lse = call.outputs()
+    call.run(attn, first, first_lse)
+    attn.check()
+    call.check(first, first_lse)
+    outs = [call.outputs() for _ in range(40)]
+    for o, lse in outs:
+        attn.workspace.fill_(0xFF)   # a NaN in every word
+        call.run(attn, o, lse)
+    attn.check()
+    for o, lse in outs:
+        assert torch.equal(o, first) and torch.equal(lse, first_lse)
