@@ -44,6 +44,7 @@ EXPORTED = (
     "gdn_tail_replay_outputs", "gdn_decode_step", "gdn_plan_create_fused", "gdn_tail_replay_prefill",
     "gdn_selftest_bounded_wait", "gdn_debug_fail_plan_allocations", "gdn_selftest_index_check",
     "gdn_debug_bounds_enabled", "gdn_qk_norm_rope", "gdn_paged_attention", "gdn_paged_attention_workspace_bytes",
+    "gdn_selftest_split_entry",
 )
 
 
@@ -139,6 +140,7 @@ def _load():
         "gdn_debug_fail_plan_allocations": (None, [I32]),
         "gdn_selftest_index_check": (I32, [P, P]),
         "gdn_debug_bounds_enabled": (I32, []),
+        "gdn_selftest_split_entry": (I32, [ctypes.POINTER(I32), I32, I32, I32, I64, I32]),
         "gdn_qk_norm_rope": (I32, [ctypes.POINTER(gdn_qk_desc), P, P, P, P, P, P, P, ctypes.c_float,
                                    ctypes.POINTER(gdn_paged_kv), P, P, P, P, P, P]),
         "gdn_paged_attention": (I32, [ctypes.POINTER(gdn_attn_desc), ctypes.POINTER(gdn_paged_kv), P, P, P, P, P, P,
@@ -386,6 +388,11 @@ def gdn_selftest_index_check(workspace, stream=None):
     """Debug build only: run one failing index check (access skipped); the workspace
     status then reads GDN_ERR_BOUNDS."""
     _check(_lib.gdn_selftest_index_check(_ptr(workspace), _stream_handle(stream)), "gdn_selftest_index_check")
+
+
+def gdn_selftest_split_entry(entry, index, parts, most_tokens, rows, num_kv_heads) -> bool:
+    """Whether the paged attention's merging kernel would merge a table entry (5 host ints) at `index`."""
+    return bool(_lib.gdn_selftest_split_entry((ctypes.c_int32 * 5)(*entry), index, parts, most_tokens, rows, num_kv_heads))
 
 
 def gdn_debug_bounds_enabled() -> bool:

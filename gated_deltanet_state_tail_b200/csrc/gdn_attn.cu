@@ -159,18 +159,15 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
     extern __shared__ __align__(16) float smem_raw[];
     SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(smem_raw);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    if (a.merge_kernel && tid == 0) a.splits[blockIdx.x].last = -1;
     const Line ln = get_line<kThreads>(a, reinterpret_cast<long long*>(smem_raw));
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if ((int)blockIdx.x >= ln.parts) {
-        if (a.merge_kernel && tid == 0) a.splits[blockIdx.x].last = -1;
-        return;
-    }
+    if ((int)blockIdx.x >= ln.parts) return;
     const long long per = ln.per_part;
     const long long start = (long long)blockIdx.x * per, end = min(start + per, ln.total);
     const StoredSeqs seqs{a};
     Unit u = find_unit(a, seqs, start);
     const float scale = a.scale * kLog2e;
-    SplitUnit goes_on{-1, 0, 0, 0, 0, {}};
     for (;; next_unit(a, seqs, u)) {
         if (start - u.begin >= u.r.tiles) {   // only the unit's extra is in this stretch
             if (unit_end(a, u) >= end) break;
@@ -525,12 +522,12 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                         merge_row<D>(a, sp, r, static_cast<float*>(a.o) + out_row(r) * D,
                                      a.lse ? a.lse + out_row(r) : nullptr);
             } else if (sp.first == (int)blockIdx.x && sp.last > sp.first) {
-                goes_on = SplitUnit{sp.last, sp.from_start, u.s.row0 + u.r.tok0, u.r.toks, u.head, {}};
+                if (tid == 0)
+                    a.splits[blockIdx.x] = SplitUnit{sp.last, sp.from_start, u.s.row0 + u.r.tok0, u.r.toks, u.head, {}};
             }
         }
         if (unit_end(a, u) >= end) break;
     }
-    if (a.merge_kernel && tid == 0) a.splits[blockIdx.x] = goes_on;
 }
 
 // The units of many rows that the cuts split: block (i, y) the one that CTA i of the
@@ -540,7 +537,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const SplitUnit u = a.splits[blockIdx.x];
     const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (u.last < 0 || r >= u.toks * a.group) return;
+    if (!to_merge(u, blockIdx.x, a.shape.max_parts, a.block_tokens, a.rows, a.num_kv_heads) || r >= u.toks * a.group) return;
     const long long row = (long long)(u.row0 + r / a.group) * a.num_heads + u.head * a.group + r % a.group;
     merge_row<D>(a, Split{(int)blockIdx.x, u.last, u.from_start != 0}, r, static_cast<float*>(a.o) + row * D,
                  a.lse ? a.lse + row : nullptr);

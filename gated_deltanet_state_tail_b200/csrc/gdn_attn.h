@@ -54,7 +54,9 @@ struct Line {
 static_assert(sizeof(Line) == 256, "Line is 256 bytes");
 
 // A unit of many rows that begins in CTA i and ends in a later one, for the merging kernel:
-// slot i of a table that every CTA writes.
+// slot i of a table that every CTA writes, "none" as it starts and the unit once it has
+// handed that out: a CTA that gives up leaves no entry of an earlier call, and no bytes that
+// the workspace happened to hold.
 struct SplitUnit {
     int last;            // its last part; -1 = there is no such unit
     int from_start;      // it begins where CTA i's stretch does
@@ -62,6 +64,14 @@ struct SplitUnit {
     int pad[3];
 };
 static_assert(sizeof(SplitUnit) == 32, "SplitUnit is 32 bytes");
+
+// Whether slot i of the table is a unit to be merged: what the merging kernel reads (parts of
+// `parts` CTAs) and writes (rows of o) by it then lies within the call's extents.
+__host__ __device__ inline bool to_merge(const SplitUnit& u, int i, int parts, int most_toks, long long rows,
+                                         int num_kv_heads) {
+    return u.last > i && u.last < parts && u.toks > 0 && u.toks <= most_toks && u.row0 >= 0 &&
+           (long long)u.row0 + u.toks <= rows && u.head >= 0 && u.head < num_kv_heads;
+}
 
 // Sizes that a kernel family fixes.
 struct Shape {

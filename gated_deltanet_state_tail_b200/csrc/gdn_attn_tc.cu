@@ -298,11 +298,9 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
             mbar_arrive(&b->piece_full[i & 1]);
         }
         __syncwarp();
-        if (a.merge_kernel && lane == 0 && !more && (p.n > 0 || i == 0)) {   // the stretch's last piece
-            const bool goes_on = p.n > 0 && !p.single && p.slot >= 0 && p.split.first == (int)blockIdx.x &&
-                                 p.split.last > p.split.first;
-            a.splits[blockIdx.x] = SplitUnit{goes_on ? p.split.last : -1, p.split.from_start, p.row0, p.toks, p.head, {}};
-        }
+        if (a.merge_kernel && lane == 0 && !more && p.n > 0 && !p.single && p.slot >= 0 &&
+            p.split.first == (int)blockIdx.x && p.split.last > p.split.first)   // the stretch's last piece goes on
+            a.splits[blockIdx.x] = SplitUnit{p.split.last, p.split.from_start, p.row0, p.toks, p.head, {}};
         for (int j = 0; j < last.n; ++j, ++tiles) {
             if (!last.tended(j)) continue;
             const int from = last.from(j), to = last.to(j);
@@ -858,12 +856,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars* b = reinterpret_cast<Bars*>(smem + S::BARS);
     const int warp = threadIdx.x >> 5;
     Line ln;
+    if (a.merge_kernel && threadIdx.x == 0) a.splits[blockIdx.x].last = -1;   // until the walker knows better
     if (a.line_inline != 2) {
         ln = get_line<kThreads>(a, reinterpret_cast<long long*>(smem + S::SCAN));
-        if ((int)blockIdx.x >= ln.parts) {
-            if (a.merge_kernel && threadIdx.x == 0) a.splits[blockIdx.x].last = -1;
-            return;
-        }
+        if ((int)blockIdx.x >= ln.parts) return;
     } else if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.ws->epoch = a.epoch;
     }
@@ -942,7 +938,7 @@ template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const SplitUnit u = a.splits[blockIdx.x];
-    if (u.last < 0) return;
+    if (!to_merge(u, blockIdx.x, a.shape.max_parts, a.block_tokens * a.shape.subs, a.rows, a.num_kv_heads)) return;
     const int s = blockIdx.y >> 2, quarter = blockIdx.y & 3, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = min(a.block_tokens, u.toks - s * a.block_tokens) * a.group;
     const int warp_rows = min(32, rows - quarter * 32);

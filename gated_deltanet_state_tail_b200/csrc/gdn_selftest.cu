@@ -3,9 +3,11 @@
 // wait site in the workspace header, and the kernel returns instead of hanging
 // or trapping, so the context stays usable and the host reads the status with
 // gdn_workspace_status().  The debug build's index checks: a failing check
-// sets kStatusBounds and skips the access it guards.
+// sets kStatusBounds and skips the access it guards.  The paged attention's
+// table of split units: what its merging kernel takes for an entry.
 #include <cuda_runtime.h>
 
+#include "gdn_attn.h"
 #include "gdn_internal.h"
 #include "gdn_sm100.h"
 #include "gdn_tail_replay.h"
@@ -58,6 +60,13 @@ extern "C" gdn_status gdn_selftest_index_check(void* workspace, void* stream) {
     gdn::index_check_selftest_kernel<<<1, 1, 0, st>>>(ws, gdn::next_call_number());
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     return GDN_OK;
+}
+
+extern "C" int32_t gdn_selftest_split_entry(const int32_t* entry, int32_t index, int32_t parts, int32_t most_tokens,
+                                            int64_t rows, int32_t num_kv_heads) {
+    if (!entry) return 0;
+    const gdn::attn::SplitUnit u{entry[0], entry[1], entry[2], entry[3], entry[4], {}};
+    return gdn::attn::to_merge(u, index, parts, most_tokens, rows, num_kv_heads) ? 1 : 0;
 }
 
 extern "C" int32_t gdn_debug_bounds_enabled(void) { return gdn::kDebugBounds ? 1 : 0; }

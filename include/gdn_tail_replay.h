@@ -520,6 +520,17 @@ GDN_API void gdn_debug_fail_plan_allocations(int32_t count);
 GDN_API int32_t gdn_debug_bounds_enabled(void);
 GDN_API gdn_status gdn_selftest_index_check(void* workspace, void* stream);
 
+/*
+ * Self-test, on the host, of the check that gdn_paged_attention's merging
+ * kernel makes of each entry of its table of split units (a call that gave up
+ * may leave any bytes there): 1 if slot `index` would be merged, else 0.
+ *   entry   {last part, begins with its part, first row, tokens, key head}
+ *   parts, most_tokens, rows, num_kv_heads
+ *           the call's extents: parts of the grid, tokens of a unit, rows of o.
+ */
+GDN_API int32_t gdn_selftest_split_entry(const int32_t* entry, int32_t index, int32_t parts, int32_t most_tokens,
+                                         int64_t rows, int32_t num_kv_heads);
+
 /* Static description of a status code. */
 GDN_API const char* gdn_status_string(gdn_status s);
 

@@ -1,0 +1,27 @@
+"""Paged attention's host-side parts that need no device."""
+import random
+
+
+import gated_deltanet_state_tail_b200 as gdn
+
+
+def test_split_table_entries_outside_the_call_are_not_merged():
+    """Whatever bytes a call that gave up leaves in the table of split units, the merging kernel reads parts and writes
+    rows of this call only."""
+    rng = random.Random(5)
+    words = [-2 ** 31, -1, 0, 1, 2, 7, 31, 127, 147, 148, 255, 4096, 0x7F7F7F7F, 2 ** 31 - 1]
+    taken = 0
+    for _ in range(20000):
+        entry = [rng.choice(words) if rng.random() < 0.5 else rng.randint(-3, 160) for _ in range(5)]
+        index, parts = rng.randrange(148), 148
+        toks, rows, heads = rng.choice([1, 2, 16, 256]), rng.choice([1, 5, 300, 2 ** 31 - 1]), rng.choice([1, 3, 8])
+        if gdn.gdn_selftest_split_entry(entry, index, parts, toks, rows, heads):
+            last, _, row0, n, head = entry
+            assert index < last < parts and 0 < n <= toks and 0 <= row0 and row0 + n <= rows and 0 <= head < heads
+            taken += 1
+    assert taken > 20
+    assert gdn.gdn_selftest_split_entry([148 - 1, 1, 44, 256, 2], 146, 148, 256, 300, 3)
+    assert not gdn.gdn_selftest_split_entry([-1, 0, 0, 1, 0], 0, 148, 256, 300, 3)          # no unit
+    assert not gdn.gdn_selftest_split_entry([3, 0, 0, 1, 0], 3, 148, 256, 300, 3)           # one part is not a split
+    assert not gdn.gdn_selftest_split_entry([148, 0, 0, 1, 0], 3, 148, 256, 300, 3)
+    assert not gdn.gdn_selftest_split_entry([5, 0, 2 ** 31 - 1, 256, 0], 3, 148, 256, 2 ** 31 - 1, 3)   # past 32 bits
