@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 // every thread has written its share
                 __threadfence();
                 __syncthreads();
-                if (__syncthreads_or(tid == 0 && (claim_arrivals(a, sp, 0), arrive_last(a, sp, 0))))
+                if (__syncthreads_or(tid == 0 && claim_arrivals(a, sp, 0) && arrive_last(a, sp, 0)))
                     for (int r = tid >> 5; r < rows; r += kWarps)
                         merge_row<D>(a, sp, r, static_cast<float*>(a.o) + out_row(r) * D,
                                      a.lse ? a.lse + out_row(r) : nullptr);

@@ -382,11 +382,14 @@ __device__ __forceinline__ Split split_of(const Unit& u, long long per) {
 // calls share one): what happens to be in fresh memory is small numbers more often than not.
 // claim_arrivals: each CTA of a split unit, before its part is counted, gives the word of
 // `share` this call's tag (and the count zero) unless another has; long before the part is
-// done, so that counting it in is a single atomic.
+// done, so that counting it in is a single atomic.  False once a launch of this call has given
+// up (a replay has its tag): its counts are then short of some parts, so nothing more is counted
+// and nothing merged from parts that are not all in.
 __device__ __forceinline__ unsigned long long arrival_tag(const Args& a) {
     return (unsigned long long)(a.epoch * 0x9E3779B1u ^ 0x5BD1E995u) << 32;
 }
-__device__ __forceinline__ void claim_arrivals(const Args& a, const Split& sp, int share) {
+__device__ __forceinline__ bool claim_arrivals(const Args& a, const Split& sp, int share) {
+    const unsigned long long status = *reinterpret_cast<volatile unsigned long long*>(&a.ws->status);
     unsigned long long* w = a.arrivals + (long long)sp.first * kArrivals + share;
     unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w);
     const unsigned long long tag = arrival_tag(a);
@@ -395,6 +398,7 @@ __device__ __forceinline__ void claim_arrivals(const Args& a, const Split& sp, i
         if (seen == old) break;
         old = seen;
     }
+    return (unsigned int)(status >> 32) != a.epoch || !((unsigned int)status & (kStatusTimeout | kStatusBounds));
 }
 
 // Counts one more part in, by one thread after its warp's (or block's) threads have written

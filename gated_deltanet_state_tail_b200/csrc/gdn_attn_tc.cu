@@ -646,7 +646,8 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
         const int all_lo = first_key(a, first_pos + toks - 1);
         const bool active = quarter * 32 < rows;   // this warp has rows
         // while the first scores are on their way
-        if (active && u.slot >= 0 && u.single && lane == 0) claim_arrivals(a, u.split, s * 4 + quarter);
+        const bool counted =
+            active && u.slot >= 0 && u.single && lane == 0 && claim_arrivals(a, u.split, s * 4 + quarter);
         __syncwarp();
         float m = -INFINITY;
         const Pair scale = pair(sl, sl);
@@ -822,7 +823,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                 // the warp that brings the last part of its half of its rows' columns merges them
                 __threadfence();
                 __syncwarp();
-                const bool last = __shfl_sync(0xffffffffu, lane == 0 && arrive_last(a, u.split, s * 4 + quarter), 0);
+                const bool last = __shfl_sync(0xffffffffu, counted && arrive_last(a, u.split, s * 4 + quarter), 0);
                 if (last) {
                     const int r = lane & (R - 1), at = quarter * 32 + r;
                     const long long orow_r = __shfl_sync(0xffffffffu, orow, r);

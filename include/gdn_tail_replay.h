@@ -379,6 +379,9 @@ GDN_API size_t gdn_paged_attention_workspace_bytes(int32_t dtype, int32_t head_d
  * do not fit is skipped (its rows stay untouched), a page number outside
  * 0 .. num_pages - 1 reads as zeros, and either sets GDN_ERR_MISMATCH in the
  * workspace status; over replays of one captured call the status accumulates.
+ * After GDN_ERR_TIMEOUT rows may be missing or wrong, and further replays of
+ * that captured call leave rows unwritten until its whole workspace is zeroed;
+ * other calls are not affected.
  * batch = 0 or rows = 0 launches nothing.  bf16 runs on the tensor cores with
  * the softmax in fp32 and its weights rounded to bf16; fp32 on the CUDA cores in
  * fp32 throughout.  Reruns give identical bits.

@@ -67,3 +67,40 @@ def test_split_units_of_few_rows_over_and_over(dtype, d, heads, kv, new):
     attn.check()
     for o, lse in outs:
         assert torch.equal(o, first) and torch.equal(lse, first_lse)
+
+
+def _words(workspace):
+    """The call number of the last launch, its arrival counts and its status word, in a workspace's header and behind it."""
+    words = workspace[:512 + 8 * 296 * 8].view(torch.int64)
+    return int(workspace[16:20].view(torch.int32)), words[512 // 8:], words[0:1]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_replays_after_a_launch_that_gave_up(dtype):
+    """Arrival counts that a launch left short, under a status that says so (both written here): a replay merges nothing
+    from parts that may not be in, keeps the status, and is right again once the workspace is zeroed."""
+    call = Call(dtype, 8, 2, 128, 16, [1, 1], [9000, 30], seed=3)
+    attn = call.attention()
+    o, lse = call.outputs()
+    call.run(attn, o, lse)
+    attn.workspace.zero_()   # so that the words that this call does not use are told from those that it does
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.run(attn, o, lse)
+    graph.replay()
+    attn.check()
+    good, good_lse = o.clone(), lse.clone()
+    call.check(good, good_lse)
+    number, counts, status = _words(attn.workspace)
+    used = counts != 0
+    assert bool(used.any()) and bool((counts[used] & 0xFFFFFFFF == 0).all())
+    counts[used] += 1
+    status.fill_((number << 32) | 2)
+    o.fill_(SENTINEL)
+    for _ in range(3):
+        graph.replay()
+        assert attn.status() == gdn.GDN_ERR_TIMEOUT
+        assert bool((o[0] == SENTINEL).all()) and torch.equal(o[1], good[1])
+    attn.workspace.zero_()
+    graph.replay()
+    assert attn.status() == gdn.GDN_OK and torch.equal(o, good) and torch.equal(lse, good_lse)
