@@ -383,6 +383,7 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
     const uint32_t base = smem_u32(smem);
     const int runs = kKeys / granule;           // TMA boxes of one 64-column block
     unsigned ring = 0, raws = 0, raw_any = 0;   // raws: parities of v_raw
+    unsigned q_loads[2] = {0, 0};
     QTiles qt;
     bool ok = true;
     Pieces pieces;
@@ -398,6 +399,7 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
             if (lane < D / 64)
                 tma_load_3d(smem + S::Q + t * S::TILE + lane * kBlock, &maps.q, &b->q_full[t], lane * 64, u.head * a.group,
                             u.row0 + (u.single ? 0 : t * a.block_tokens));
+            ++q_loads[t];
         }
         if (!ok) break;
         qt.next(u);
@@ -445,14 +447,15 @@ __device__ __forceinline__ void load_role(const Args& a, const Maps& maps, uint8
             }
         }
     }
-    if (!ok) {   // wait for this warp's own copies before the CTA may leave
-        const unsigned n = min(ring, (unsigned)S::STAGES);
-        for (unsigned i = ring - n; i < ring; ++i) mbar_wait_bounded(&b->kv_full[i % S::STAGES], (i / S::STAGES) & 1, kWaitNs);
-        for (int i = 0; i < S::STAGES; ++i)
-            if ((raw_any >> i) & 1) mbar_wait_bounded(&b->v_raw[i], ((raws >> i) & 1) ^ 1, kWaitNs);
-        for (int t = 0; t < 2; ++t)
-            if (qt.uses[t]) mbar_wait_bounded(&b->q_full[t], (qt.uses[t] - 1) & 1, kWaitNs);
-    }
+    // This warp's copies are in before the CTA may leave, whichever way the loop ended: another
+    // role may give up, now or later, with some of them on their way.  (The products wait for
+    // the same copies, so this delays nothing.)
+    const unsigned n = min(ring, (unsigned)S::STAGES);
+    for (unsigned i = ring - n; i < ring; ++i) mbar_wait_bounded(&b->kv_full[i % S::STAGES], (i / S::STAGES) & 1, kWaitNs);
+    for (int i = 0; i < S::STAGES; ++i)
+        if ((raw_any >> i) & 1) mbar_wait_bounded(&b->v_raw[i], ((raws >> i) & 1) ^ 1, kWaitNs);
+    for (int t = 0; t < 2; ++t)
+        if (q_loads[t]) mbar_wait_bounded(&b->q_full[t], (q_loads[t] - 1) & 1, kWaitNs);
 }
 
 // --------------------------------------------------------------- MMA issuers

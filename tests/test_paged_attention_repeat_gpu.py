@@ -104,3 +104,32 @@ def test_replays_after_a_launch_that_gave_up(dtype):
     attn.workspace.zero_()
     graph.replay()
     assert attn.status() == gdn.GDN_OK and torch.equal(o, good) and torch.equal(lse, good_lse)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("batch,rows", [(1, 1), (3, 40), (40, 700)])
+def test_nothing_but_empty_sequences(dtype, batch, rows):
+    """No sequence has a new token: every CTA ends without a piece of work, and the rows stay."""
+    call = Call(dtype, 4, 2, 128, 16, [rows] + [0] * (batch - 1), [max(rows, 50)] * batch, seed=batch)
+    attn = call.attention()
+    o, lse = call.outputs()
+    call.run(attn, o, lse, cu=_i32([0] * (batch + 1)))
+    attn.check()
+    assert bool((o == SENTINEL).all()) and bool((lse == SENTINEL).all())
+    call.run(attn, o, lse)
+    attn.check()
+    call.check(o, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ctx", [1, 128, 129, 640, 641, 1280, 1281, 3000])
+@pytest.mark.parametrize("new", [1, 16, 40])
+def test_every_copy_is_in_before_a_block_ends(d, ctx, new):
+    """Pieces of one tile to more than the ring of copies holds, with and without tended value tiles, one after the other
+    over the same rings: each copy's barrier completes as often as it is waited for."""
+    call = Call(BF16, 8, 1, d, 16, [min(new, ctx)] * 3, [ctx] * 3, seed=ctx + new)
+    attn = call.attention()
+    o, lse = call.outputs()
+    call.run(attn, o, lse)
+    attn.check()
+    call.check(o, lse)
