@@ -438,6 +438,8 @@ def _row_stride(shape, stride, name):
     rows, heads, dim = shape
     if rows and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
         raise ValueError(f"{name} must have contiguous heads inside a row")
+    if rows > 1 and stride[0] == 0:   # the descriptors' 0 means packed rows
+        raise ValueError(f"{name} must not be one row expanded to many")
     return stride[0] if rows > 1 else 0
 
 
@@ -484,6 +486,8 @@ def _kv_desc(shape, stride, packed, code):
     if len(shape) != 4 or stride[3] != 1:
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, num_kv_heads, head_dim] with contiguous "
                          "elements inside a head")
+    if any(n > 1 and s == 0 for n, s in zip(shape, stride)):   # the descriptor's three zeros mean packed
+        raise ValueError("k_cache and v_cache must not be expanded")
     return gdn_paged_kv(*shape, code, 0, *((0, 0, 0) if packed else stride[:3]))
 
 

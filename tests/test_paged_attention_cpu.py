@@ -1,6 +1,9 @@
 """Paged attention's host-side parts that need no device."""
 import random
 
+import pytest
+import torch
+
 
 import gated_deltanet_state_tail_b200 as gdn
 
@@ -25,3 +28,27 @@ def test_split_table_entries_outside_the_call_are_not_merged():
     assert not gdn.gdn_selftest_split_entry([3, 0, 0, 1, 0], 3, 148, 256, 300, 3)           # one part is not a split
     assert not gdn.gdn_selftest_split_entry([148, 0, 0, 1, 0], 3, 148, 256, 300, 3)
     assert not gdn.gdn_selftest_split_entry([5, 0, 2 ** 31 - 1, 256, 0], 3, 148, 256, 2 ** 31 - 1, 3)   # past 32 bits
+
+
+def test_expanded_rows_are_refused():
+    """A stride of 0 is the descriptors' word for packed rows: one row expanded to many would be read past its end."""
+    x = torch.zeros(8, 128)
+    for rows in (2, 4096):
+        y = x[None].expand(rows, 8, 128)
+        with pytest.raises(ValueError, match="q must not"):
+            gdn._row_stride(y.shape, y.stride(), "q")
+    one = x[None].expand(1, 8, 128)
+    assert gdn._row_stride(one.shape, one.stride(), "q") == 0
+    wide = torch.zeros(4, 12, 128)[:, :8]
+    assert gdn._row_stride(wide.shape, wide.stride(), "q") == 12 * 128
+
+
+@pytest.mark.parametrize("shape", [(3, 16, 2, 128), (3, 1, 1, 128), (1, 16, 1, 128), (1, 1, 2, 128), (3, 16, 1, 128)])
+def test_expanded_caches_are_refused(shape):
+    row = torch.zeros(128).expand(*shape)
+    with pytest.raises(ValueError, match="expanded"):
+        gdn._paged_kv(row, row)
+    pages = torch.zeros(16, 2, 128)[None].expand(3, 16, 2, 128)
+    with pytest.raises(ValueError, match="expanded"):
+        gdn._paged_kv(pages, pages)
+    assert gdn._paged_kv(torch.zeros(shape), torch.zeros(shape)).page_stride == 0

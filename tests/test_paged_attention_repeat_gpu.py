@@ -133,3 +133,26 @@ def test_every_copy_is_in_before_a_block_ends(d, ctx, new):
     call.run(attn, o, lse)
     attn.check()
     call.check(o, lse)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_expanded_tensors_are_refused(dtype):
+    """Through the public calls: nothing is launched, nothing written."""
+    call = Call(dtype, 4, 2, 128, 16, [5], [30], seed=9)
+    attn = call.attention()
+    o, _ = call.outputs()
+    call.q = call.q[:1].expand(5, 4, 128)
+    with pytest.raises(ValueError):
+        call.run(attn, o)
+    x = torch.randn((5, 8, 128), device="cuda").to(dtype)
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    pos, inv = torch.arange(5, device="cuda"), torch.ones(64, dtype=torch.float64, device="cuda")
+    cache = dict(v=v, k_cache=call.cache.k, v_cache=call.cache.v, slots=pos)
+    before = call.cache.k.clone()
+    for kw in (dict(q=q[:1].expand_as(q), k=k, **cache), dict(q=q, k=k[:1].expand_as(k), **cache),
+               dict(q=q, k=k, **dict(cache, v=v[:1].expand_as(v))),
+               dict(q=q, k=k, **dict(cache, k_cache=x[0, 0].expand(3, 16, 2, 128), v_cache=x[0, 0].expand(3, 16, 2, 128)))):
+        with pytest.raises(ValueError):
+            gdn.qk_norm_rope(positions=pos, inv_freq=inv, **kw)
+    torch.cuda.synchronize()
+    assert bool((o == SENTINEL).all()) and torch.equal(call.cache.k.nan_to_num(), before.nan_to_num())
