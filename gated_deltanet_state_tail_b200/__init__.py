@@ -233,6 +233,8 @@ def row_stride_of(*tensors) -> int:
     for t in ts:
         if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
             raise ValueError("q/k/v must be [rows, H, d] views with contiguous heads inside a row")
+        if t.shape[0] > 1 and t.stride(0) == 0:   # 0 would read as packed
+            raise ValueError("q, k and v must not be one row expanded to many")
     if all(t.stride(0) == t.shape[1] * t.shape[2] for t in ts):
         return 0
     rs = {t.stride(0) for t in ts}

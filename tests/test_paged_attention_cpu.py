@@ -43,6 +43,19 @@ def test_expanded_rows_are_refused():
     assert gdn._row_stride(wide.shape, wide.stride(), "q") == 12 * 128
 
 
+def test_expanded_rows_of_a_plan_call_are_refused():
+    x = torch.zeros(4, 128)
+    for dtype in (torch.float32, torch.bfloat16):
+        y = x.to(dtype)[None].expand(50, 4, 128)
+        with pytest.raises(ValueError, match="expanded"):
+            gdn.row_stride_of(y, y)
+        with pytest.raises(ValueError, match="expanded"):
+            gdn.row_stride_of(torch.zeros(50, 4, 128, dtype=dtype), y)
+    assert gdn.row_stride_of(x[None], None, x[None]) == 0
+    wide = torch.zeros(5, 3, 4, 128)
+    assert gdn.row_stride_of(wide[:, 0], wide[:, 1], wide[:, 2]) == 3 * 4 * 128
+
+
 @pytest.mark.parametrize("shape", [(3, 16, 2, 128), (3, 1, 1, 128), (1, 16, 1, 128), (1, 1, 2, 128), (3, 16, 1, 128)])
 def test_expanded_caches_are_refused(shape):
     row = torch.zeros(128).expand(*shape)
