@@ -150,7 +150,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return y;
 }
 
-// 2^y of both halves on the FMA pipe, for y < 128; exactly 0 at and below -127.  y = n + f
+// 2^y of both halves on the FMA pipe, for y < 128; exactly 0 at and below -127, and for NaN (a
+// row with one is NaN by its other exponentials and its offset).  y = n + f
 // with n the nearest integer (found by adding 1.5 * 2^23, whose low bits then hold it), 2^f a
 // polynomial of degree 5 with value 1 at 0 and else the least relative error on [-1/2, 1/2]
 // (a Remez fit of its own: 4.9e-7 in fp32 arithmetic, twice the special function unit's),
@@ -711,7 +712,11 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                         }
                     }
                 }
-                const float off = m == -INFINITY ? 0.0f : -m * sl;
+                // An infinite maximum (a score of +infinity, or finite ones beyond fp32 once scaled)
+                // has no softmax: 0 x off makes the offset, and so every exponential of the row, NaN.
+                // The polynomial's clamp would turn the NaN of infinity - infinity into 0.
+                float off = m == -INFINITY ? 0.0f : -m * sl;
+                off = fmaf(off, 0.0f, off);
                 probabilities<kPoly>(x, scale, pair(off, off), tm_s, sum);
                 tmem_wait_st();
             }

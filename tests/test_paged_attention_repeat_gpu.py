@@ -156,3 +156,51 @@ def test_expanded_tensors_are_refused(dtype):
             gdn.qk_norm_rope(positions=pos, inv_freq=inv, **kw)
     torch.cuda.synchronize()
     assert bool((o == SENTINEL).all()) and torch.equal(call.cache.k.nan_to_num(), before.nan_to_num())
+
+
+def _poke(call, b, key, head, column, value):
+    page = call.cache.k.shape[1]
+    call.cache.k[int(call.cache.table[b, key // page]), key % page, head, column] = value
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d,heads,new,ctx", [(128, 2, 200, 200), (64, 2, 200, 200), (128, 8, 300, 300), (64, 8, 70, 150),
+                                             (128, 16, 64, 4000), (128, 2, 3, 3000), (64, 8, 1, 130)])
+def test_infinite_scores_make_a_row_nan(dtype, d, heads, new, ctx):
+    """A key with an infinity scores +infinity with the rows whose query has its sign there: their softmax is NaN, at every
+    position of a step and of the last one, in whole and in split units.  With the other sign the key has weight 0."""
+    call = Call(dtype, heads, 2, d, 16, [new], [ctx], seed=d + new)
+    call.q[..., 5] = torch.where(torch.arange(new, device="cuda")[:, None] % 3 == 0, -1.0, 1.0).to(dtype)
+    attn = call.attention()
+    good, good_lse = call.outputs()
+    call.run(attn, good, good_lse)
+    group, pos = heads // 2, torch.arange(ctx - new, ctx, device="cuda")
+    keys = sorted({k for k in [*range(ctx - 70, ctx), *range(60, 70), 0, 1, 500, 1999] if 0 <= k < ctx})
+    for key in keys:
+        page, row = int(call.cache.table[0, key // 16]), key % 16
+        was = call.cache.k[page, row, 1].clone()
+        _poke(call, 0, key, 1, 5, math.inf)
+        o, lse = call.outputs()
+        call.run(attn, o, lse)
+        call.cache.k[page, row, 1] = was
+        nan = (pos >= key) & (torch.arange(new, device="cuda") % 3 != 0)
+        assert bool(torch.isnan(o[nan, group:]).all()) and bool(torch.isnan(lse[nan, group:]).all()), key
+        rest = ~nan & ((pos > 0) | (key > 0))   # a row with no other key has no softmax either
+        assert bool(torch.isfinite(o[rest]).all()) and bool(torch.isfinite(lse[rest]).all()), key
+        assert torch.equal(o[:, :group], good[:, :group]) and torch.equal(o[pos < key], good[pos < key])
+    attn.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new,ctx", [(200, 200), (1, 300), (40, 40)])
+def test_scores_beyond_fp32_do_not_vanish(dtype, new, ctx):
+    """Finite products that overflow fp32 once scaled: NaN, as an infinite score, not a row of zeros."""
+    call = Call(dtype, 4, 2, 128, 16, [new], [ctx], seed=17)
+    call.q.fill_(2.0 ** 60)
+    for key in range(ctx):
+        _poke(call, 0, key, slice(None), slice(None), 1.0)
+    attn = call.attention()
+    o, lse = call.outputs()
+    call.run(attn, o, lse, scale=2.0 ** 66)
+    attn.check()
+    assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
