@@ -5,7 +5,7 @@
 // and query head h, over the keys j in (p - window, p], j >= 0, of key head h / group:
 //   o = sum_j softmax_j(scale q . k_j) v_j,    lse = log sum_j exp(scale q . k_j)
 // in one pass over the keys with a running maximum and sum.  A row without keys gives
-// o = 0 and lse = -infinity.
+// o = 0 and lse = -infinity; one whose scores are all -infinity o = NaN and the same lse.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -116,7 +116,7 @@ __device__ __forceinline__ void copies_wait() {
 // Row r of a split unit merged by a warp, its columns over the lanes, eight parts read at
 // once; every part has the weight 2^(its log-sum).
 template <int D>
-__device__ __forceinline__ void merge_row(const Args& a, const Split& sp, int r, float* to, float* lse) {
+__device__ __forceinline__ void merge_row(const Args& a, const Split& sp, int r, bool sees, float* to, float* lse) {
     constexpr int AHEAD = 8;
     const int lane = threadIdx.x & 31, col = 4 * lane;
     float top = -INFINITY, sum = 0.0f;
@@ -148,7 +148,7 @@ __device__ __forceinline__ void merge_row(const Args& a, const Split& sp, int r,
             acc.w = fmaf(f, x[i].w, acc.w);
         }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a NaN part makes the row NaN
+    const float inv = inverse_sum(sum, sees);   // a NaN part makes the row NaN
     if (col < D)
         *reinterpret_cast<float4*>(to + col) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (lse && lane == 0) *lse = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 if (lane == 0) {
                     const float lse2 = sum == 0.0f ? -INFINITY : m[j] + log2f(sum);
-                    sm.inv()[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    sm.inv()[r] = inverse_sum(sum, whole && first_pos + r / a.group >= 0);
                     if (!whole) a.part_lse[part_slot(blockIdx.x, begins) * kRows + r] = lse2;
                     else if (a.lse) a.lse[out_row(r)] = lse2 * kLn2;
                 }
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                     float sum = l[i];
 #pragma unroll
                     for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    const float inv = inverse_sum(sum, whole && top_key[i] >= 0);
                     const float lse2 = sum == 0.0f ? -INFINITY : m[i] + log2f(sum);
                     const int r = kTR * ty + i;
                     if (r >= rows) continue;
@@ -519,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const Args a) {
                 __syncthreads();
                 if (__syncthreads_or(tid == 0 && claim_arrivals(a, sp, 0) && arrive_last(a, sp, 0)))
                     for (int r = tid >> 5; r < rows; r += kWarps)
-                        merge_row<D>(a, sp, r, static_cast<float*>(a.o) + out_row(r) * D,
+                        merge_row<D>(a, sp, r, first_pos + r / a.group >= 0, static_cast<float*>(a.o) + out_row(r) * D,
                                      a.lse ? a.lse + out_row(r) : nullptr);
             } else if (sp.first == (int)blockIdx.x && sp.last > sp.first) {
                 if (tid == 0)
-                    a.splits[blockIdx.x] = SplitUnit{sp.last, sp.from_start, u.s.row0 + u.r.tok0, u.r.toks, u.head, {}};
+                    a.splits[blockIdx.x] = SplitUnit{sp.last, sp.from_start, u.s.row0 + u.r.tok0, u.r.toks, u.head, first_pos, {}};
             }
         }
         if (unit_end(a, u) >= end) break;
@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args a) {
     const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
     if (!to_merge(u, blockIdx.x, a.shape.max_parts, a.block_tokens, a.rows, a.num_kv_heads) || r >= u.toks * a.group) return;
     const long long row = (long long)(u.row0 + r / a.group) * a.num_heads + u.head * a.group + r % a.group;
-    merge_row<D>(a, Split{(int)blockIdx.x, u.last, u.from_start != 0}, r, static_cast<float*>(a.o) + row * D,
-                 a.lse ? a.lse + row : nullptr);
+    merge_row<D>(a, Split{(int)blockIdx.x, u.last, u.from_start != 0}, r, u.first_pos + r / a.group >= 0,
+                 static_cast<float*>(a.o) + row * D, a.lse ? a.lse + row : nullptr);
 }
 
 template <int D>

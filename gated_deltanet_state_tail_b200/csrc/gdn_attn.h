@@ -61,7 +61,8 @@ struct SplitUnit {
     int last;            // its last part; -1 = there is no such unit
     int from_start;      // it begins where CTA i's stretch does
     int row0, toks, head;
-    int pad[3];
+    int first_pos;       // position of its first token
+    int pad[2];
 };
 static_assert(sizeof(SplitUnit) == 32, "SplitUnit is 32 bytes");
 
@@ -114,6 +115,14 @@ struct Args {
     float* part_lse;                        // [2 * max_parts][subs * sub_rows], base 2
     float* part_o;                          // [2 * max_parts] slots of subs * sub_rows * dim values
 };
+
+// What a row's outputs are multiplied by, given the sum of its weights.  A row that sees no key
+// has the sum 0 and gets zeros; one that sees keys has it only if every score is -infinity, and
+// such a row has no softmax.  Parts decide nothing: `sees` is for
+// whole rows and merged ones.
+__device__ __forceinline__ float inverse_sum(float sum, bool sees) {
+    return sum != 0.0f ? 1.0f / sum : sees ? __int_as_float(0x7fffffff) : 0.0f;   // a NaN sum stays
+}
 
 __device__ __forceinline__ void report(const Args& a, unsigned int bits) {
     tag_merge(&a.ws->status, a.epoch, bits, false);

@@ -301,7 +301,7 @@ __device__ __forceinline__ void walk_role(const Args& a, const Line& ln, const S
         __syncwarp();
         if (a.merge_kernel && lane == 0 && !more && p.n > 0 && !p.single && p.slot >= 0 &&
             p.split.first == (int)blockIdx.x && p.split.last > p.split.first)   // the stretch's last piece goes on
-            a.splits[blockIdx.x] = SplitUnit{p.split.last, p.split.from_start, p.row0, p.toks, p.head, {}};
+            a.splits[blockIdx.x] = SplitUnit{p.split.last, p.split.from_start, p.row0, p.toks, p.head, p.first_pos, {}};
         for (int j = 0; j < last.n; ++j, ++tiles) {
             if (!last.tended(j)) continue;
             const int from = last.from(j), to = last.to(j);
@@ -550,6 +550,7 @@ struct Merge {
     long long offset;
     int stride;
     bool mine;                // the lane has a row
+    bool sees;                // and that sees a key
     int groups, first, step;
 
     template <int GROUPS, int PARTS>
@@ -600,7 +601,7 @@ struct Merge {
                     }
                 }
             }
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a NaN part makes the row NaN
+            const float inv = inverse_sum(sum, sees);   // a NaN part makes the row NaN
             if (lse_out && g0 == 0) *lse_out = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
@@ -757,7 +758,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                 f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - top) * sl);
                 sum = l0 * f0 + l1 * f1;
             }
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = inverse_sum(sum, whole && top_key >= 0);
             f0 *= inv;
             f1 *= inv;
             // single: this group takes half of the columns, of both streams
@@ -836,7 +837,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, uint8_t* smem, Bars*
                     const int r = lane & (R - 1), at = quarter * 32 + r;
                     const long long orow_r = __shfl_sync(0xffffffffu, orow, r);
                     const Merge<D> mg{a, u.split, s * kRows + at, warp_at + 4 * r, 4 * R, at < rows,
-                                      D / 8, lane >> log_r, 32 >> log_r};
+                                      first_pos + at / a.group >= 0, D / 8, lane >> log_r, 32 >> log_r};
                     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.o) + orow_r * D + s * (D / 2);
                     float* lse = a.lse && at < rows && lane < R && s == 0 ? a.lse + orow_r : nullptr;
                     // few rows have few columns a lane, so as many more parts in flight (20 parts of 4
@@ -959,7 +960,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args a) {
     const Split sp{(int)blockIdx.x, u.last, u.from_start != 0};
     const int step = 32 >> log_r;
     const Merge<D> mg{a, sp, s * kRows + at, (long long)(s * 4 + quarter) * 32 * D + 4 * r, 4 * R, at < rows,
-                      D / 4, (lane >> log_r) + warp * step, 8 * step};
+                      u.first_pos + s * a.block_tokens + at / a.group >= 0, D / 4, (lane >> log_r) + warp * step, 8 * step};
     float* lse = a.lse && at < rows && lane < R && warp == 0 ? a.lse + row : nullptr;
     mg.template run<4, 6>(static_cast<__nv_bfloat16*>(a.o) + row * D, lse);
 }

@@ -65,7 +65,7 @@ extern "C" gdn_status gdn_selftest_index_check(void* workspace, void* stream) {
 extern "C" int32_t gdn_selftest_split_entry(const int32_t* entry, int32_t index, int32_t parts, int32_t most_tokens,
                                             int64_t rows, int32_t num_kv_heads) {
     if (!entry) return 0;
-    const gdn::attn::SplitUnit u{entry[0], entry[1], entry[2], entry[3], entry[4], {}};
+    const gdn::attn::SplitUnit u{entry[0], entry[1], entry[2], entry[3], entry[4], 0, {}};
     return gdn::attn::to_merge(u, index, parts, most_tokens, rows, num_kv_heads) ? 1 : 0;
 }
 

@@ -362,7 +362,8 @@ GDN_API size_t gdn_paged_attention_workspace_bytes(int32_t dtype, int32_t head_d
  * sees the keys j of max(0, p - window + 1) .. p (window 0: 0 .. p):
  *   o = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j).
  * A row that sees no key (L = 0, or more rows than context) gets o = 0 and
- * lse = -infinity.  Cache rows outside the context or before every row's window
+ * lse = -infinity; a row whose scores are all -infinity has no softmax (o = NaN,
+ * lse = -infinity).  Cache rows outside the context or before every row's window
  * are not used, whatever they hold, and page numbers of pages that hold only
  * such rows are not read.  Infinities and NaN in q, k and v reach only the rows
  * that see them: padding behind a sequence's tokens may hold anything.

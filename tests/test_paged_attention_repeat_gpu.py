@@ -204,3 +204,37 @@ def test_scores_beyond_fp32_do_not_vanish(dtype, new, ctx):
     call.run(attn, o, lse, scale=2.0 ** 66)
     attn.check()
     assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d,heads,new,ctx,window", [(128, 2, 200, 200, 0), (64, 8, 300, 300, 0), (128, 8, 40, 40, 0),
+                                                    (128, 8, 300, 2000, 7), (64, 2, 3, 3000, 0), (128, 2, 1, 4000, 0),
+                                                    (128, 4, 600, 3000, 0), (64, 8, 30, 20, 0)])
+def test_rows_of_scores_of_minus_infinity_are_nan(dtype, d, heads, new, ctx, window):
+    """-infinity for every key that a row sees is no softmax: o = NaN, lse = -infinity.  Beside other keys it is weight 0,
+    bit for bit as a score far below theirs.  Rows without keys stay zero."""
+    call = Call(dtype, heads, 2, d, 16, [new], [ctx], seed=d + new + 1)
+    call.q[..., 5] = 1.0
+    attn = call.attention()
+    group, pos = heads // 2, torch.arange(ctx - new, ctx, device="cuda")
+    keys = torch.arange(ctx, device="cuda")
+    at = call.cache.table[0][keys // 16].long(), keys % 16
+    was = call.cache.k.clone()
+    for low, high in ((0, min(ctx, 10)), (ctx // 2, ctx // 2 + 9), (0, ctx // 2), (0, ctx - 1), (0, ctx)):
+        got = {}
+        hit = (keys >= low) & (keys < high)
+        for value in (-math.inf, -4096.0):
+            call.cache.k.copy_(was)
+            call.cache.k[at[0][hit], at[1][hit], 1, 5] = value
+            o, lse = call.outputs()
+            call.run(attn, o, lse, window=window)
+            got[value] = o, lse
+        first = (pos - (window or ctx) + 1).clamp_min(0)
+        gone = (pos >= 0) & (first >= low) & (pos < high)
+        (o, lse), (far, far_lse) = got[-math.inf], got[-4096.0]
+        assert bool(torch.isnan(o[gone, group:]).all()) and bool((lse[gone, group:] == -math.inf).all())
+        assert torch.equal(o[~gone], far[~gone]) and torch.equal(lse[~gone], far_lse[~gone])
+        assert torch.equal(o[:, :group], far[:, :group])
+        assert bool((o[pos < 0] == 0).all()) and bool((lse[pos < 0] == -math.inf).all())
+        assert bool(torch.isfinite(far).all())
+    attn.check()
