@@ -577,8 +577,14 @@ def _attention_bytes(code, dim, batch):
 def gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace, scale=None,
                         window=0, stream=None):
     """Causal attention of new tokens over a paged cache (see ``PagedAttention.run``)."""
-    torch = _torch()
     device = _launch_device(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace)
+    _attend(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace, scale, window,
+            _launch_stream(stream, device))
+
+
+def _attend(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace, scale, window, stream):
+    """gdn_paged_attention on tensors of the current device and a raw stream."""
+    torch = _torch()
     c = _paged_kv(k_cache, v_cache)
     q_shape, t_shape = q.shape, page_table.shape
     if len(q_shape) != 3 or q.dtype is not k_cache.dtype:
@@ -604,8 +610,7 @@ def gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len
                    dim ** -0.5 if scale is None else scale)
     status = _fn("gdn_paged_attention")(
         ctypes.byref(d), ctypes.byref(c), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-        cu_seqlens.data_ptr(), context_len.data_ptr(), o_out.data_ptr(), lse_ptr, workspace.data_ptr(),
-        _launch_stream(stream, device))
+        cu_seqlens.data_ptr(), context_len.data_ptr(), o_out.data_ptr(), lse_ptr, workspace.data_ptr(), stream)
     if status:
         _check(status, "gdn_paged_attention")
 
@@ -728,7 +733,8 @@ def decode_step(q, k, v, alpha, beta, state, o=None, in_place=True):
 
 class PagedAttention:
     """Causal attention of new tokens over a paged key/value cache, with the workspace that its calls share
-    (calls that may run at the same time, or captured ones that may, need one each).
+    (calls that may run at the same time, or captured ones that may, need one each; it lives as long as graphs that
+    captured its calls).
 
     Lengths and pages are device tensors read when the call runs, so a captured ``run`` may be replayed with new
     ones.  The cache already holds the new tokens (``qk_norm_rope`` appends them).
@@ -744,6 +750,9 @@ class PagedAttention:
             raise GdnError(GDN_ERR_UNSUPPORTED, "PagedAttention")
         self.workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
         self.workspace[:256].zero_()   # the status, for status() before the first run
+        made_on = torch.cuda.current_stream()
+        self._made = None if torch.cuda.is_current_stream_capturing() else made_on.record_event()
+        self._ordered = {made_on.cuda_stream}   # streams that are behind the workspace's making
 
     def run(self, q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out=None, scale=None, window=0,
             stream=None, workspace=None):
@@ -756,8 +765,25 @@ class PagedAttention:
             raise ValueError("q or the cache has other heads than this PagedAttention")
         if page_table.shape[0] > self.max_batch or (self.max_rows is not None and rows > self.max_rows):
             raise ValueError("more sequences or rows than this PagedAttention was made for")
-        gdn_paged_attention(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out,
-                            self.workspace if workspace is None else workspace, scale, window, stream)
+        if workspace is None:
+            workspace = self.workspace
+        device = _launch_device(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace)
+        handle = _launch_stream(stream, device)
+        if handle not in self._ordered and workspace is self.workspace:
+            self._order(stream, handle)
+        _attend(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse_out, workspace, scale, window, handle)
+
+    def _order(self, stream, handle):
+        """The first run on a stream other than the one that the workspace was made on: behind what that one had
+        queued then (the memory's earlier owner, the zeroed status), and with the memory kept until this stream is done
+        with it.  torch.cuda.graph waits for the device before it captures, and the caller keeps what it captured."""
+        torch = _torch()
+        if self._made is None or torch.cuda.is_current_stream_capturing():
+            return
+        stream = torch.cuda.current_stream() if stream is None else stream
+        stream.wait_event(self._made)
+        self.workspace.record_stream(stream)
+        self._ordered.add(handle)
 
     def status(self, stream=None) -> int:
         return gdn_workspace_status(self.workspace, stream)

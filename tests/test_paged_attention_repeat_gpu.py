@@ -238,3 +238,56 @@ def test_rows_of_scores_of_minus_infinity_are_nan(dtype, d, heads, new, ctx, win
         assert bool((o[pos < 0] == 0).all()) and bool((lse[pos < 0] == -math.inf).all())
         assert bool(torch.isfinite(far).all())
     attn.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("how", ["argument", "current"])
+def test_first_run_on_another_stream_than_the_workspace(dtype, how):
+    """The workspace is made on one stream behind long work there, and first used on another: the call comes after its
+    making, so that what the call reports is not wiped."""
+    call = Call(dtype, 8, 2, 128, 16, [1, 20], [500, 90], seed=23)
+    o, lse = call.outputs()
+    call.run(call.attention(), o, lse)
+    bad = call.cache.table.clone()
+    bad[1, 1] = -1
+    wrong, wrong_lse = call.outputs()
+    again, again_lse = call.outputs()
+    side = torch.cuda.Stream()
+    a = torch.randn((8192, 8192), device="cuda", dtype=BF16)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a @ a   # some 15 ms
+    attn = call.attention()
+    if how == "argument":
+        call.run(attn, wrong, wrong_lse, table=bad, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            call.run(attn, wrong, wrong_lse, table=bad)
+    torch.cuda.synchronize()
+    assert attn.status() == gdn.GDN_ERR_MISMATCH
+    call.run(attn, again, again_lse, stream=side)
+    assert attn.status(side) == gdn.GDN_OK
+    assert torch.equal(again, o) and torch.equal(again_lse, lse)
+
+
+def test_workspace_outlives_its_calls_on_another_stream():
+    """A PagedAttention that is dropped while its call waits on another stream: the memory is not handed out meanwhile."""
+    call = Call(BF16, 8, 1, 128, 16, [1], [30000], seed=24)
+    o, lse = call.outputs()
+    call.run(call.attention(), o, lse)
+    got, got_lse = call.outputs()
+    side = torch.cuda.Stream()
+    a = torch.randn((8192, 8192), device="cuda", dtype=BF16)
+    attn = call.attention()
+    size, at = attn.workspace.numel(), attn.workspace.data_ptr()
+    call.run(attn, got, got_lse, stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            a @ a
+    call.run(attn, got, got_lse, stream=side)
+    del attn
+    taken = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(t.data_ptr() != at for t in taken)
+    torch.cuda.synchronize()
+    assert torch.equal(got, o) and torch.equal(got_lse, lse)
