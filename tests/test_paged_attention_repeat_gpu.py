@@ -291,3 +291,110 @@ def test_workspace_outlives_its_calls_on_another_stream():
     assert all(t.data_ptr() != at for t in taken)
     torch.cuda.synchronize()
     assert torch.equal(got, o) and torch.equal(got_lse, lse)
+
+
+def test_reruns_of_fp32_give_the_same_bits():
+    call = Call(F32, 8, 2, 128, 16, [1, 33, 260], [3000, 900, 2600], seed=41)
+    attn = call.attention()
+    first, first_lse = call.outputs()
+    call.run(attn, first, first_lse)
+    call.check(first, first_lse)
+    for _ in range(10):
+        attn.workspace.fill_(0xFF)
+        o, lse = call.outputs()
+        call.run(attn, o, lse)
+        attn.check()
+        assert torch.equal(o, first) and torch.equal(lse, first_lse)
+
+
+def test_bad_descriptors_of_fp32_are_reported_and_skipped():
+    """A page number outside the pool, a context past the table, offsets that decrease or leave the rows, for units of few
+    rows and of many."""
+    call = Call(F32, 4, 2, 128, 16, [20, 3, 1], [200, 90, 500], seed=61)
+    attn = call.attention()
+    good, good_lse = call.outputs()
+    call.run(attn, good, good_lse)
+    attn.check()
+    for bad in (-1, call.cache.pages, 2 ** 31 - 1, -2 ** 31):
+        for b, mine in ((0, slice(0, 20)), (1, slice(20, 23)), (2, slice(23, 24))):
+            table = call.cache.table.clone()
+            table[b, 2] = bad
+            o, _ = call.outputs()
+            call.run(attn, o, table=table)
+            assert attn.status() == gdn.GDN_ERR_MISMATCH
+            other = torch.ones(24, dtype=torch.bool, device="cuda")
+            other[mine] = False
+            assert torch.equal(o[other], good[other]) and bool(torch.isfinite(o[mine]).all())
+    width = call.cache.table.shape[1] * 16
+    for c in (width + 1, 2 ** 31 - 1, -1):
+        o, _ = call.outputs()
+        call.run(attn, o, ctx=_i32([200, c, 500]))
+        assert attn.status() == gdn.GDN_ERR_MISMATCH
+        assert bool((o[20:23] == SENTINEL).all()) and torch.equal(o[:20], good[:20]) and torch.equal(o[23:], good[23:])
+    for offsets in ([0, 20, 23, 25], [0, 20, 23, 2 ** 31 - 1], [0, 20, 10, 24], [-1, 20, 23, 24]):
+        o, _ = call.outputs()
+        call.run(attn, o, cu=_i32(offsets))
+        assert attn.status() == gdn.GDN_ERR_MISMATCH
+    o, lse = call.outputs()
+    call.run(attn, o, lse)
+    assert attn.status() == gdn.GDN_OK and torch.equal(o, good) and torch.equal(lse, good_lse)
+
+
+def test_captured_fp32_calls_follow_new_lengths():
+    call = Call(F32, 8, 2, 128, 16, [1, 4, 20], [900, 60, 333], seed=71, width=80)
+    ctx = _i32([5, 4, 20])
+    attn, eager = call.attention(), call.attention()
+    o, lse = call.outputs()
+    call.run(attn, o, lse, ctx=ctx)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.run(attn, o, lse, ctx=ctx)
+    for lens in ([900, 60, 333], [17, 4, 100], [640, 33, 20], [900, 60, 333]):
+        ctx.copy_(_i32(lens))
+        for _ in range(3):
+            o.fill_(SENTINEL)
+            graph.replay()
+        attn.check()
+        want, want_lse = call.outputs()
+        call.run(eager, want, want_lse, ctx=ctx)
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+        call.check(o, lse, lens)
+
+
+def test_two_fp32_calls_at_once():
+    call = Call(F32, 8, 2, 128, 64, [1, 130, 2], [9000, 800, 5000], seed=81)
+    want, want_lse = call.outputs()
+    call.run(call.attention(), want, want_lse)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    attns = [call.attention() for _ in range(2)]
+    outs = [call.outputs() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, a, (o, lse) in zip(streams, attns, outs):
+            call.run(a, o, lse, stream=s)
+    torch.cuda.synchronize()
+    for s, a, (o, lse) in zip(streams, attns, outs):
+        assert a.status(s) == gdn.GDN_OK and torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_graphs_that_share_a_workspace_take_turns(dtype):
+    """Two captured calls and an eager one of other shapes through one workspace, one after the other."""
+    calls = [Call(dtype, 8, 2, 128, 16, new, ctx, seed=51 + n) for n, (new, ctx) in
+             enumerate([([1, 1], [9000, 70]), ([2, 5], [400, 3000]), ([300], [2500])])]
+    attn = calls[0].attention()
+    outs, want = [c.outputs() for c in calls], [c.outputs() for c in calls]
+    graphs = []
+    for c, (o, lse), w in zip(calls, outs, want):
+        c.run(c.attention(), *w)
+        c.run(attn, o, lse)
+        if c is not calls[2]:
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                c.run(attn, o, lse)
+    for turn in range(6):
+        for n in ((0, 1, 2), (2, 1, 0), (1, 1, 0))[turn % 3]:
+            outs[n][0].fill_(SENTINEL)
+            graphs[n].replay() if n < 2 else calls[2].run(attn, *outs[2])
+            assert attn.status() == gdn.GDN_OK
+            assert torch.equal(outs[n][0], want[n][0]) and torch.equal(outs[n][1], want[n][1])
