@@ -471,6 +471,15 @@ def _launch_stream(stream, device):
     return raw(device) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
+def _refused(status, what, **tensors):
+    """Raises for a call's status, naming the tensors that start off a 16-byte boundary: a slice of an index array
+    (``positions[1:]``) is the likeliest refusal that a program meets."""
+    off = [name for name, t in tensors.items() if t is not None and t.data_ptr() % 16]
+    if status == GDN_ERR_INVALID_ARG and off:
+        what = f"{what}: {', '.join(off)} must start on a 16-byte boundary"
+    raise GdnError(status, what)
+
+
 _entry = {}
 
 
@@ -562,7 +571,8 @@ def gdn_qk_norm_rope(q, k, v, positions, inv_freq, q_weight, k_weight, eps, k_ca
         ctypes.byref(d), q.data_ptr(), k.data_ptr(), v_ptr, pos_ptr, freq_ptr, qw_ptr, kw_ptr, eps, cache, slot_ptr,
         k_pages, v_pages, q_out.data_ptr(), ko_ptr, _launch_stream(stream, device))
     if status:
-        _check(status, "gdn_qk_norm_rope")
+        _refused(status, "gdn_qk_norm_rope", q=q, k=k, v=v, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
+                 k_weight=k_weight, k_cache=k_cache, v_cache=v_cache, slots=slots, q_out=q_out, k_out=k_out)
 
 
 def gdn_paged_attention_workspace_bytes(dtype, head_dim, max_batch) -> int:
@@ -612,7 +622,8 @@ def _attend(q, k_cache, v_cache, page_table, cu_seqlens, context_len, o_out, lse
         ctypes.byref(d), ctypes.byref(c), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
         cu_seqlens.data_ptr(), context_len.data_ptr(), o_out.data_ptr(), lse_ptr, workspace.data_ptr(), stream)
     if status:
-        _check(status, "gdn_paged_attention")
+        _refused(status, "gdn_paged_attention", q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table,
+                 cu_seqlens=cu_seqlens, context_len=context_len, o_out=o_out, lse_out=lse_out, workspace=workspace)
 
 
 class _Plan:
@@ -759,7 +770,8 @@ class PagedAttention:
         """q [rows, H, d] (row-strided views too); k_cache, v_cache [num_pages, page_size, Hkv, d]; page_table
         [B, max_pages], cu_seqlens [B + 1], context_len [B] int32; o_out [rows, H, d] and lse_out [rows, H] fp32
         are written at the rows that sequences own.  Row i of a sequence with n new tokens and context L is
-        position L - n + i and sees the keys up to it, with a window only the last `window` of them."""
+        position L - n + i and sees the keys up to it, with a window only the last `window` of them.  Every tensor
+        starts on a 16-byte boundary (copy an odd slice of an index array)."""
         rows, heads, dim = q.shape
         if heads != self.num_heads or dim != self.head_dim or k_cache.shape[2] != self.num_kv_heads:
             raise ValueError("q or the cache has other heads than this PagedAttention")
@@ -810,8 +822,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     2 * inv_freq.numel() elements by position * inv_freq (fp64, radians), and, with a paged cache, the append of
     keys and values at `slots` (int64 page * page_size + row; a negative one writes nothing).
 
-    q, k and v are [rows, heads, d] (row-strided views too).  Returns (q_out, k_out); k_out is made only where
-    there is no cache and none was given."""
+    q, k and v are [rows, heads, d] (row-strided views too).  Every tensor starts on a 16-byte boundary (copy an odd
+    slice of an index array).  Returns (q_out, k_out); k_out is made only where there is no cache and none was given."""
     if q_out is None or (k_out is None and k_cache is None):
         torch = _torch()
         with torch.cuda.stream(stream):   # what is made here is made on the stream that fills it

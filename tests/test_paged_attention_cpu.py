@@ -65,3 +65,15 @@ def test_expanded_caches_are_refused(shape):
     with pytest.raises(ValueError, match="expanded"):
         gdn._paged_kv(pages, pages)
     assert gdn._paged_kv(torch.zeros(shape), torch.zeros(shape)).page_stride == 0
+
+
+def test_refusals_name_misaligned_tensors():
+    x = torch.zeros(8, dtype=torch.int64)
+    x = x[(-x.data_ptr() // 8) % 2:]
+    with pytest.raises(gdn.GdnError, match="positions, slots must start on a 16-byte") as e:
+        gdn._refused(gdn.GDN_ERR_INVALID_ARG, "call", q=x, positions=x[1:], k_out=None, slots=x[3:4])
+    assert e.value.status == gdn.GDN_ERR_INVALID_ARG
+    for status, tensors in ((gdn.GDN_ERR_INVALID_ARG, dict(q=x)), (gdn.GDN_ERR_CUDA, dict(q=x[1:]))):
+        with pytest.raises(gdn.GdnError) as e:
+            gdn._refused(status, "call", **tensors)
+        assert "boundary" not in str(e.value) and e.value.status == status

@@ -398,3 +398,18 @@ def test_graphs_that_share_a_workspace_take_turns(dtype):
             graphs[n].replay() if n < 2 else calls[2].run(attn, *outs[2])
             assert attn.status() == gdn.GDN_OK
             assert torch.equal(outs[n][0], want[n][0]) and torch.equal(outs[n][1], want[n][1])
+
+
+def test_misaligned_index_arrays_are_refused_by_name():
+    call = Call(BF16, 4, 2, 128, 16, [1, 1, 1], [30, 40, 50], seed=9)
+    attn = call.attention()
+    o, _ = call.outputs()
+    longer = _i32([0] + call.ctx)
+    with pytest.raises(gdn.GdnError, match="context_len must start"):
+        call.run(attn, o, ctx=longer[1:])
+    call.run(attn, o, ctx=longer[1:].clone())
+    attn.check()
+    x = torch.randn((3, 8, 128), device="cuda").to(BF16)
+    pos, inv = torch.arange(4, device="cuda"), torch.ones(64, dtype=torch.float64, device="cuda")
+    with pytest.raises(gdn.GdnError, match="positions, slots must start"):
+        gdn.qk_norm_rope(x[:, :4], x[:, 4:6], pos[1:], inv, v=x[:, 6:], k_cache=call.cache.k, v_cache=call.cache.v, slots=pos[1:])
