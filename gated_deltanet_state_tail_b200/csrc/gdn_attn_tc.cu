@@ -49,6 +49,10 @@ constexpr int kStep = 64;          // keys of a softmax step
 constexpr int kThreads = 384;      // softmax groups: warps 0-3 and 4-7; MMA: 8 and 9; loader: 10; walker: 11
 constexpr int kMaxParts = 148;     // one CTA per SM of a B200
 constexpr uint64_t kWaitNs = 1000000000ull;
+// A role waits for another through up to two units of the longest context (the walker for the
+// tended tiles at a unit's end, while the loader is at its beginning): what a tile may take
+// beyond kWaitNs.  A tile takes 2 us when all SMs share the HBM bandwidth.
+constexpr uint64_t kWaitNsPerTile = 8192;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a row's maximum that P absorbs
 constexpr int kPoly = 5;           // of 16 pairs of exponentials, those on the FMA pipe; a prompt of 4096
@@ -101,6 +105,7 @@ struct Bars {
     uint32_t tmem;
     int abort;             // a wait ran out
     int bad_page;
+    uint64_t limit_ns;     // of a wait for another role
 };
 static_assert(sizeof(Bars) <= 704, "the barriers fit their space");
 
@@ -115,7 +120,7 @@ __device__ __forceinline__ bool wait_one(Bars* b, uint64_t* bar, uint32_t parity
         const uint64_t t0 = global_timer_ns();
         while (!(done = mbar_try_wait(bar, parity))) {
             if (*reinterpret_cast<volatile int*>(&b->abort)) break;
-            if (global_timer_ns() - t0 > kWaitNs) {
+            if (global_timer_ns() - t0 > b->limit_ns) {
                 *reinterpret_cast<volatile int*>(&b->abort) = 1;   // reported at the end
                 break;
             }
@@ -899,6 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b->v_clean[i], 1);
         }
         b->abort = b->bad_page = 0;
+        b->limit_ns = kWaitNs + kWaitNsPerTile * (min((long long)kMostKeys, (long long)a.max_pages * a.page_size) / kKeys);
         mbar_fence_init();
     }
     if (warp == 8) {

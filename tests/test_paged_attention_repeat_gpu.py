@@ -413,3 +413,24 @@ def test_misaligned_index_arrays_are_refused_by_name():
     pos, inv = torch.arange(4, device="cuda"), torch.ones(64, dtype=torch.float64, device="cuda")
     with pytest.raises(gdn.GdnError, match="positions, slots must start"):
         gdn.qk_norm_rope(x[:, :4], x[:, 4:6], pos[1:], inv, v=x[:, 6:], k_cache=call.cache.k, v_cache=call.cache.v, slots=pos[1:])
+
+
+def test_a_unit_of_more_than_a_second():
+    """One token over 250 million keys (few pages, again and again), a key head per CTA: a unit takes longer than the
+    second that a wait may take for short contexts.  Values are not compared: fp32 sums of as many terms are not exact."""
+    heads, d, page, pages, times = 148, 64, 256, 4, 250_000
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    k, v = (torch.randn((pages, page, heads, d), generator=g, device="cuda").to(BF16) for _ in range(2))
+    q = torch.randn((1, heads, d), generator=g, device="cuda").to(BF16)
+    attn = gdn.PagedAttention(heads, heads, d, BF16, max_batch=1)
+    got = []
+    for n in (1, times):
+        table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(n)[None]
+        o, lse = torch.full_like(q, SENTINEL), torch.full((1, heads), SENTINEL, device="cuda")
+        attn.run(q, k, v, table, _i32([0, 1]), _i32([n * pages * page]), o, lse)
+        assert attn.status() == gdn.GDN_OK
+        got.append((o.float(), lse))
+    assert bool(torch.isfinite(got[1][0]).all())
+    # a rounded sum of positive terms never shrinks: at least one repeat's log-sum, up to its own 1024 roundings
+    assert bool((got[1][1] >= got[0][1] - 1e-3).all())
