@@ -4,8 +4,8 @@
 
 produces gated_deltanet_state_tail_b200/libgdn_tail_replay.so from csrc/*.cu,
 and the debug build libgdn_tail_replay_debug.so (-DGDN_DEBUG_BOUNDS: every
-kernel checks the global indices it computes against the plan's extents and
-reports GDN_ERR_BOUNDS instead of accessing out of range).
+kernel that takes a plan checks the global indices it computes against the plan's
+extents and reports GDN_ERR_BOUNDS instead of accessing out of range).
 """
 from __future__ import annotations
 

@@ -55,8 +55,10 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kWaitNsPerTile = 8192;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;      // log2 of the growth of a row's maximum that P absorbs
-constexpr int kPoly = 5;           // of 16 pairs of exponentials, those on the FMA pipe; a prompt of 4096
-                                   // tokens takes 98, 97, 95, 96 and 98 us with 0, 3, 5, 6 and 8
+// Of 16 pairs of exponentials, those on the FMA pipe.  0, 3, 5 and 8 in turn, 200 calls in a row,
+// medians of 15: a 4096-token prompt of 16 heads 101, 96, 94 and 99 us; 512 tokens behind 8K 53.5,
+// 51.4, 51.3 and 53.3; 1024 behind 32K, 32 heads, 670, 620, 626 and 661 (spread of one: 3 %).
+constexpr int kPoly = 5;
 constexpr int kBlock = kKeys * 128;   // bytes of one 64-column block of a 128-row tile
 
 template <int D>
@@ -159,7 +161,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // row with one is NaN by its other exponentials and its offset).  y = n + f
 // with n the nearest integer (found by adding 1.5 * 2^23, whose low bits then hold it), 2^f a
 // polynomial of degree 5 with value 1 at 0 and else the least relative error on [-1/2, 1/2]
-// (a Remez fit of its own: 4.9e-7 in fp32 arithmetic, twice the special function unit's),
+// (a Remez fit of its own: 4.9e-7 in fp32 arithmetic against 2^f in fp64, twice the special
+// function unit's error),
 // n added to its exponent: -127 leaves none of 1.0's.
 __device__ __forceinline__ float2 ex2_poly(Pair y) {
     const float2 in = unpair(y);

@@ -18,11 +18,12 @@
 // 170 and 172 us with one, two and eight.  The result is rounded once, from fp32, when it
 // is stored.
 //
-// The angle is exact for far positions without a table and without fp64 per pair: a
+// The angle holds for far positions without a table and without fp64 per pair: a
 // turn is 2^64, so p f_i mod 2 pi is the low 64 bits of p times the frequency in turns
 // as a 64-bit fraction, one integer product that wraps by itself.  The fraction comes
-// from the fp64 frequency (error below 2^-52 of f), its signed value is rounded to fp32
-// (2^-24 of a half turn) and goes to sincospif.  A block computes the cosines and sines
+// from the fp64 frequency (error below 2^-52 of f, and 2^-64 of a turn where it is cut off;
+// both times p), its signed value is rounded to fp32 (2^-24 of a half turn, which hides them
+// up to p = 2^28) and goes to sincospif.  A block computes the cosines and sines
 // of its rows once, in shared memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -310,8 +310,10 @@ typedef struct gdn_qk_desc {
  * Norm and rotation of the new tokens' queries and keys, and their append to
  * the cache, in one pass.  Per head: y = x rsqrt(mean(x^2) + eps) w, then each
  * pair (a, b) of the rotated elements turns by t = position * inv_freq:
- * (a cos t - b sin t, b cos t + a sin t).  Computed in fp32 and rounded once;
- * angles are exact to fp32 at any position (no table).
+ * (a cos t - b sin t, b cos t + a sin t).  Computed in fp32 and rounded once.
+ * There is no table: t comes from a 64-bit product, off by at most 2^-52 of
+ * itself and 2^-61 radians a position, below fp32's own rounding at positions up
+ * to 2^28.
  *   q            [rows, num_heads, head_dim] (row stride of the descriptor)
  *   k, v         [rows, num_kv_heads, head_dim]; v with a cache only.
  *   positions    [rows] int64;  inv_freq [rotary_dim / 2] fp64, radians per
@@ -515,6 +517,8 @@ GDN_API void gdn_debug_fail_plan_allocations(int32_t count);
  * the extents the plan validated on the host.  A failing check skips the
  * access and sets GDN_ERR_BOUNDS in the workspace status; nothing traps.
  * The decode step has no workspace: its indices come from its grid alone.
+ * gdn_paged_attention and gdn_qk_norm_rope have no such checks: in every build
+ * they compare lengths, offsets, page numbers and slots with the call's extents.
  * gdn_debug_bounds_enabled() returns 1 in the debug build, 0 otherwise.
  * gdn_selftest_index_check() runs one failing check (on an index one past a
  * 4-element extent, access skipped) so that gdn_workspace_status() then

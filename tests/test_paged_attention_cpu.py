@@ -1,6 +1,9 @@
 """Paged attention's host-side parts that need no device."""
+import os
 import random
+import re
 
+import numpy as np
 import pytest
 import torch
 
@@ -77,3 +80,19 @@ def test_refusals_name_misaligned_tensors():
         with pytest.raises(gdn.GdnError) as e:
             gdn._refused(status, "call", **tensors)
         assert "boundary" not in str(e.value) and e.value.status == status
+
+
+def test_polynomial_exponential():
+    """2^f on [-1/2, 1/2] by the kernel's coefficients, in fp32 with fused multiply-adds (an fp64 product of two fp32
+    values is exact), against fp64: the error that the kernel states."""
+    path = os.path.join(os.path.dirname(gdn.__file__), "csrc", "gdn_attn_tc.cu")
+    body = open(path).read().split("float2 ex2_poly(Pair y)")[1].split("const float2 e =")[0]
+    c = [np.float32(x) for x in re.findall(r"pair\(([0-9.]+)f, \1f\)", body.split("Pair p =")[1])]
+    assert len(c) == 6 and c[-1] == 1
+    f = np.linspace(-0.5, 0.5, 200001).astype(np.float32)
+    p = np.full_like(f, c[0])
+    for x in c[1:]:
+        p = (p.astype(np.float64) * f + np.float64(x)).astype(np.float32)
+    want = np.exp2(f.astype(np.float64))
+    assert float(np.abs(p / want - 1).max()) <= 4.9e-7
+    assert p[np.flatnonzero(f == 0)[0]] == 1
